@@ -185,7 +185,7 @@ def _logits(shape, g, dtype, sharp):
     x = torch.randn(shape, generator=g, device=DEV).mul_(2.0)
     likely = torch.randint(0, shape[-1], (*shape[:-1], 6), generator=g, device=DEV)
     up = torch.rand((*shape[:-1], 6), generator=g, device=DEV).mul_(sharp).add_(6.0)
-    return x.scatter_(-1, likely, up).to(dtype)
+    return x.scatter_reduce_(-1, likely, up, "amax").to(dtype)  # a column drawn twice: the larger, whatever the order
 
 
 def _prepare_logprobs(c, g):
