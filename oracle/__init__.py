@@ -44,3 +44,4 @@ from .attention import (  # noqa: F401
     window_positions,
 )
 from .ring import RingModel  # noqa: F401
+from .step import PageModel, accept_sequence, rotate_heads, row_logprobs, top_tokens  # noqa: F401

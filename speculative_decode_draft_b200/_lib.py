@@ -1,4 +1,4 @@
-"""ctypes binding of libwmtp (include/wmtp.h): argument marshalling only.
+"""ctypes binding of libwmtp (include/wmtp.h, wmtp_step.h, wmtp_pool.h): argument marshalling only.
 
 Every computation happens in the CUDA kernels behind the C ABI.  PyTorch is
 used for device memory and streams.  If the shared library is missing, every
@@ -14,7 +14,7 @@ from ctypes import POINTER, c_float, c_int32, c_size_t, c_void_p
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwmtp.so")
 
-# status codes and device status bits (include/wmtp.h)
+# status codes and device status bits (include/wmtp.h, include/wmtp_step.h)
 WMTP_OK = 0
 WMTP_ERR_INVALID_ARG = -1
 WMTP_ERR_UNSUPPORTED = -2
@@ -26,6 +26,13 @@ DEV_RING_STATE = 0x4
 DEV_UNDO_FULL = 0x8
 DEV_TIMEOUT = 0x10
 DEV_V_RANGE = 0x20  # reserved, never set
+DEV_POOL = 0x40
+DEV_LOGITS = 0x80
+DEV_TOKEN_OOB = 0x100
+# wmtp_dtype
+DTYPE_BF16 = 0
+DTYPE_FP16 = 1
+DTYPE_FP32 = 2
 WAIT_LIMIT_CYCLES = 4000000000  # WMTP_WAIT_LIMIT_CYCLES
 
 EXPORTS = (
@@ -49,6 +56,10 @@ EXPORTS = (
     "wmtp_pool_release",
     "wmtp_plan_admission",
     "wmtp_selftest_wait",
+    "wmtp_qk_norm_rope",
+    "wmtp_pages_resize",
+    "wmtp_token_logprobs",
+    "wmtp_accept_draft",
 )
 
 # Size of the fixed scratch array behind wmtp_draft_attn_full_noalloc.
@@ -90,6 +101,15 @@ class RingDesc(ctypes.Structure):
         ("undo_v", c_void_p),
         ("undo_tags", c_void_p),
         ("batch", c_int32),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("turn", c_void_p),
+        ("rotary_dim", c_int32),
+        ("interleaved", c_int32),
+        ("factor", c_float),
     ]
 
 
@@ -180,6 +200,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                         POINTER(Admission)]
     lib.wmtp_selftest_wait.restype = c_int32
     lib.wmtp_selftest_wait.argtypes = [c_int32, c_void_p, c_void_p, c_void_p]
+    i64 = ctypes.c_int64
+    lib.wmtp_qk_norm_rope.restype = c_int32
+    lib.wmtp_qk_norm_rope.argtypes = [PP, POINTER(RopeDesc), c_int32, c_int32, c_void_p, i64, i64, c_void_p, i64,
+                                      i64, c_void_p, i64, i64, c_void_p, c_void_p, PK, c_void_p, c_void_p, c_int32,
+                                      c_float, c_float, c_void_p, c_void_p, i32p, c_void_p]
+    lib.wmtp_pages_resize.restype = c_int32
+    lib.wmtp_pages_resize.argtypes = [PP, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_int32, c_void_p, c_void_p, c_void_p, c_int32, i32p, c_void_p]
+    lib.wmtp_token_logprobs.restype = c_int32
+    lib.wmtp_token_logprobs.argtypes = [c_int32, c_int32, c_int32, c_void_p, i64, c_void_p, c_void_p, c_int32,
+                                        c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, i32p, c_void_p]
+    lib.wmtp_accept_draft.restype = c_int32
+    lib.wmtp_accept_draft.argtypes = [c_int32, c_int32, c_int32, c_int32, c_void_p, i64, i64, c_void_p, i64, i64,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, sz, i32p, c_void_p]
     if path is None:
         _lib = lib
     return lib

@@ -57,6 +57,7 @@
 #include <stdint.h>
 
 #include "ptx.cuh"
+#include "status.cuh"
 
 namespace wmtp {
 
@@ -68,13 +69,6 @@ constexpr int kComputeThreads = 32 * kComputeWarps;
 constexpr int kPPitchBytes = 144;  // one P row: 64 bf16 + 16 bytes of padding
 constexpr int kBarCompute = 1;     // named barrier id of the compute warps
 constexpr int kRunTiles = 256;     // tiles per accumulation run (16,384 tokens)
-
-// Status bits (mirror include/wmtp.h).
-constexpr int kDevPageOob = 0x1;
-constexpr int kDevLenOob = 0x2;
-constexpr int kDevRingState = 0x4;
-constexpr int kDevUndoFull = 0x8;
-constexpr int kDevTimeout = 0x10;
 
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [B][num_q][Hq][D]
@@ -107,10 +101,6 @@ struct DecodeArgs {
   __nv_bfloat16* k_pool_w;
   __nv_bfloat16* v_pool_w;
 };
-
-__device__ __forceinline__ void set_status(int32_t* status, int bits) {
-  if (status != nullptr) atomicOr(status, bits);
-}
 
 // ---------------------------------------------------------------- smem plan
 template <int D, int NT, int STAGES>

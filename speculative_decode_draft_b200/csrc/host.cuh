@@ -1,0 +1,72 @@
+// Host-side helpers shared by the files that define the C ABI: alignment,
+// device information, launches, supported page sizes.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <utility>
+
+#include "wmtp.h"
+
+namespace wmtp {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kWsAlign = 256;
+constexpr int kMaxGridYZ = 65535;       // gridDim.y / gridDim.z limit
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// ---------------------------------------------------------------- device info
+struct DeviceInfo {
+  int sms = 0;
+};
+
+DeviceInfo g_dev[kMaxDevices];
+std::once_flag g_dev_once[kMaxDevices];
+
+wmtp_status current_device(int* dev, DeviceInfo* info) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return WMTP_ERR_CUDA;
+  const int d = *dev;
+  std::call_once(g_dev_once[d], [d]() {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d) == cudaSuccess) g_dev[d].sms = sms;
+  });
+  if (g_dev[d].sms <= 0) return WMTP_ERR_CUDA;
+  *info = g_dev[d];
+  return WMTP_OK;
+}
+
+// ---------------------------------------------------------------- launches
+// A launch whose success is read from the launch call itself, never from
+// cudaGetLastError (which would also report an unrelated earlier error left
+// on this thread, after the kernel had been queued).  `programmatic`: launch
+// as a programmatic dependent of the previous work on the stream (the kernel
+// must execute griddepcontrol.wait before its first memory access).
+template <typename... Exp, typename... Act>
+wmtp_status launch_plain(bool programmatic, void (*kern)(Exp...), dim3 grid, dim3 block, cudaStream_t st,
+                         Act&&... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = programmatic ? attr : nullptr;
+  cfg.numAttrs = programmatic ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...) == cudaSuccess ? WMTP_OK : WMTP_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- shapes
+bool supported_page(int p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
+
+}  // namespace
+}  // namespace wmtp

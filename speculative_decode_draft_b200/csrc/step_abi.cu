@@ -1,0 +1,222 @@
+// libwmtp: the C ABI declared in include/wmtp_step.h.
+//
+// Host side only: argument validation, workspace sizing and kernel launches.
+// The work runs in the kernels of rope.cuh, pages.cuh and logits.cuh.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <initializer_list>
+
+#include "host.cuh"
+#include "logits.cuh"
+#include "pages.cuh"
+#include "rope.cuh"
+#include "wmtp_step.h"
+
+namespace wmtp {
+namespace {
+
+constexpr int kMaxVocab = 1 << 30;
+constexpr int kMaxAcceptQ = 32;
+constexpr long long kMaxGridX = 0x7fffffffLL;
+
+bool dtype_bytes(int32_t dtype, int* bytes) {
+  *bytes = dtype == WMTP_FP32 ? 4 : 2;
+  return dtype == WMTP_BF16 || dtype == WMTP_FP16 || dtype == WMTP_FP32;
+}
+
+bool words_ok(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
+
+// A [tokens][heads][D] view that 16-byte loads can read.
+bool heads_ok(const void* p, int64_t token_stride, int64_t head_stride, int bytes) {
+  return aligned(p, 16) && token_stride >= 0 && head_stride >= 0 && token_stride * bytes % 16 == 0 &&
+         head_stride * bytes % 16 == 0;
+}
+
+}  // namespace
+}  // namespace wmtp
+
+using namespace wmtp;
+
+extern "C" {
+
+wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, int32_t tokens, int32_t in_dtype,
+                              const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                              int64_t v_head_stride, const int32_t* positions, const int64_t* slots,
+                              const wmtp_paged_kv* kv, const void* q_weight, const void* k_weight,
+                              int32_t weight_dtype, float weight_offset, float eps, void* q_out, void* k_out,
+                              int32_t* status_word, void* stream) {
+  if (params == nullptr || tokens < 0) return WMTP_ERR_INVALID_ARG;
+  const int D = params->head_dim;
+  if (params->num_heads_q <= 0 || params->num_heads_kv <= 0) return WMTP_ERR_INVALID_ARG;
+  if (params->num_heads_q > kMaxGridYZ || params->num_heads_kv > kMaxGridYZ) return WMTP_ERR_UNSUPPORTED;
+  if (D <= 0 || D % 8 != 0 || D > kRopeMaxDim) return WMTP_ERR_UNSUPPORTED;
+  if (in_dtype != WMTP_BF16 && in_dtype != WMTP_FP32) return WMTP_ERR_UNSUPPORTED;
+  if (weight_dtype != WMTP_BF16 && weight_dtype != WMTP_FP32) return WMTP_ERR_UNSUPPORTED;
+  if (!std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.f) return WMTP_ERR_INVALID_ARG;
+  if (rope != nullptr) {
+    if (rope->rotary_dim < 0 || rope->rotary_dim > D || rope->rotary_dim % 2 != 0) return WMTP_ERR_INVALID_ARG;
+    if (rope->rotary_dim > 0 && rope->turn == nullptr) return WMTP_ERR_INVALID_ARG;
+    if (!std::isfinite(rope->factor) || !aligned(rope->turn, 8)) return WMTP_ERR_INVALID_ARG;
+  }
+  // queries have a place to go, keys one at least, values the cache
+  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr && k == nullptr)) return WMTP_ERR_INVALID_ARG;
+  if (k == nullptr ? (k_out != nullptr || slots != nullptr) : (k_out == nullptr && slots == nullptr))
+    return WMTP_ERR_INVALID_ARG;
+  if ((slots == nullptr) != (v == nullptr)) return WMTP_ERR_INVALID_ARG;
+  if (slots != nullptr) {
+    if (!supported_page(params->page_size)) return WMTP_ERR_UNSUPPORTED;
+    if (kv == nullptr || kv->k_pool == nullptr || kv->v_pool == nullptr || kv->num_pages <= 0 ||
+        !aligned(kv->k_pool, 16) || !aligned(kv->v_pool, 16) || !aligned(slots, 8))
+      return WMTP_ERR_INVALID_ARG;
+  }
+  if (tokens == 0) return WMTP_OK;
+  if (positions == nullptr || !aligned(positions, 4)) return WMTP_ERR_INVALID_ARG;
+  const int bytes = in_dtype == WMTP_FP32 ? 4 : 2;
+  if (!heads_ok(q, q_token_stride, q_head_stride, bytes) || !heads_ok(k, k_token_stride, k_head_stride, bytes) ||
+      !heads_ok(v, v_token_stride, v_head_stride, bytes))
+    return WMTP_ERR_INVALID_ARG;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return WMTP_ERR_INVALID_ARG;
+  RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q, a.k = k, a.v = v;
+  a.q_token = q_token_stride, a.q_head = q_head_stride;
+  a.k_token = k_token_stride, a.k_head = k_head_stride;
+  a.v_token = v_token_stride, a.v_head = v_head_stride;
+  a.positions = positions;
+  a.slots = slots;
+  if (slots != nullptr) {
+    a.k_pool = static_cast<__nv_bfloat16*>(kv->k_pool);
+    a.v_pool = static_cast<__nv_bfloat16*>(kv->v_pool);
+    a.num_slots = static_cast<long long>(kv->num_pages) * params->page_size;
+    a.page_size = params->page_size;
+  }
+  a.qw = q_weight, a.kw = k_weight;
+  a.weight_f32 = weight_dtype == WMTP_FP32;
+  a.offset = weight_offset, a.eps = eps;
+  if (rope != nullptr) {
+    a.turn = rope->turn;
+    a.rotary_dim = rope->rotary_dim;
+    a.interleaved = rope->interleaved != 0;
+    a.factor = rope->factor;
+  }
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.tokens = tokens, a.Hq = params->num_heads_q, a.Hkv = params->num_heads_kv, a.D = D;
+  a.status = status_word;
+  const int rows = (q != nullptr ? a.Hq : 0) + (k != nullptr ? a.Hkv : 0) + (v != nullptr ? a.Hkv : 0);
+  const long long grid = (static_cast<long long>(tokens) * rows + kRopeWarps - 1) / kRopeWarps;
+  if (grid > kMaxGridX) return WMTP_ERR_UNSUPPORTED;
+  auto kern = in_dtype == WMTP_FP32 ? rope_kernel<float> : rope_kernel<__nv_bfloat16>;
+  return launch_plain(true, kern, dim3(static_cast<unsigned>(grid)), dim3(kRopeThreads),
+                      static_cast<cudaStream_t>(stream), a);
+}
+
+wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t* page_table, int32_t max_pages,
+                              int32_t* kv_len, const int32_t* new_len, int32_t* free_pages, int32_t* free_count,
+                              int32_t num_pages, int32_t* cu_tokens, int32_t* positions, int64_t* slots,
+                              int32_t max_tokens, int32_t* status_word, void* stream) {
+  if (params == nullptr || batch < 0 || max_tokens < 0) return WMTP_ERR_INVALID_ARG;
+  if (!supported_page(params->page_size) || batch > kMaxGridYZ) return WMTP_ERR_UNSUPPORTED;
+  if (max_pages <= 0 || num_pages <= 0) return WMTP_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * params->page_size > (1LL << 30)) return WMTP_ERR_UNSUPPORTED;
+  const bool map = max_tokens > 0;
+  if (map != (cu_tokens != nullptr) || map != (positions != nullptr) || map != (slots != nullptr))
+    return WMTP_ERR_INVALID_ARG;
+  if (free_pages == nullptr || free_count == nullptr || (batch > 0 && (page_table == nullptr || kv_len == nullptr ||
+                                                                       new_len == nullptr)))
+    return WMTP_ERR_INVALID_ARG;
+  if (!words_ok({page_table, kv_len, new_len, free_pages, free_count, cu_tokens, positions}) || !aligned(slots, 8))
+    return WMTP_ERR_INVALID_ARG;
+  if (batch == 0 && !map) return WMTP_OK;
+  PagesArgs a;
+  a.page_table = page_table, a.kv_len = kv_len, a.new_len = new_len;
+  a.free_pages = free_pages, a.free_count = free_count;
+  a.cu = cu_tokens, a.positions = positions, a.slots = slots;
+  a.status = status_word;
+  a.B = batch, a.max_pages = max_pages, a.P = params->page_size, a.num_pages = num_pages, a.max_tokens = max_tokens;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  wmtp_status s = launch_plain(true, pages_kernel, dim3(1), dim3(kPagesThreads), st, a);
+  if (s != WMTP_OK || !map) return s;
+  return launch_plain(true, slots_kernel, dim3((max_tokens + kSlotThreads - 1) / kSlotThreads), dim3(kSlotThreads), st,
+                      a);
+}
+
+wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, const void* logits, int64_t row_stride,
+                                const float* temperature, const int32_t* tokens, int32_t num_tokens, int32_t top_k,
+                                float* logprobs_out, float* entropy_out, float* lse_out, float* top_logprobs_out,
+                                int32_t* top_ids_out, int32_t* status_word, void* stream) {
+  int bytes = 0;
+  if (rows < 0 || vocab <= 0 || num_tokens < 0 || top_k < 0) return WMTP_ERR_INVALID_ARG;
+  if (!dtype_bytes(dtype, &bytes) || vocab > kMaxVocab || top_k > kMaxTop) return WMTP_ERR_UNSUPPORTED;
+  if (row_stride < vocab && rows > 1) return WMTP_ERR_INVALID_ARG;
+  if (num_tokens > 0 && rows > 0 && (tokens == nullptr || logprobs_out == nullptr)) return WMTP_ERR_INVALID_ARG;
+  if (top_k > 0 && rows > 0 && (top_logprobs_out == nullptr || top_ids_out == nullptr)) return WMTP_ERR_INVALID_ARG;
+  if (rows == 0) return WMTP_OK;
+  if (logits == nullptr || !aligned(logits, bytes)) return WMTP_ERR_INVALID_ARG;
+  if (!words_ok({temperature, tokens, logprobs_out, entropy_out, lse_out, top_logprobs_out, top_ids_out}))
+    return WMTP_ERR_INVALID_ARG;
+  LogprobArgs a;
+  a.logits = logits, a.row_stride = row_stride, a.temperature = temperature, a.tokens = tokens;
+  a.logprobs = logprobs_out, a.entropy = entropy_out, a.lse = lse_out, a.top_logprobs = top_logprobs_out;
+  a.top_ids = top_ids_out, a.status = status_word;
+  a.V = vocab, a.num_tokens = num_tokens, a.top_k = top_k;
+  auto kern = dtype == WMTP_FP32   ? logprob_kernel<float>
+              : dtype == WMTP_FP16 ? logprob_kernel<__half>
+                                   : logprob_kernel<__nv_bfloat16>;
+  return launch_plain(true, kern, dim3(rows), dim3(kRowThreads), static_cast<cudaStream_t>(stream), a);
+}
+
+wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32_t dtype, const void* target,
+                              int64_t target_batch_stride, int64_t target_row_stride, const void* draft,
+                              int64_t draft_batch_stride, int64_t draft_row_stride, const int32_t* draft_tokens,
+                              const float* uniforms, const int32_t* num_draft, const float* temperature,
+                              int32_t* tokens_out, int32_t* count_out, float* logprobs_out, void* workspace,
+                              size_t* workspace_bytes, int32_t* status_word, void* stream) {
+  int bytes = 0;
+  if (batch < 0 || num_q <= 0 || vocab <= 0 || workspace_bytes == nullptr) return WMTP_ERR_INVALID_ARG;
+  if (!dtype_bytes(dtype, &bytes) || vocab > kMaxVocab || num_q > kMaxAcceptQ || batch > kMaxGridYZ)
+    return WMTP_ERR_UNSUPPORTED;
+  const size_t need = align_up(static_cast<size_t>(batch) * (2 * num_q - 1) * sizeof(RowStat), kWsAlign);
+  if (workspace == nullptr) {
+    *workspace_bytes = need;
+    return WMTP_OK;
+  }
+  if (*workspace_bytes < need || !aligned(workspace, kWsAlign)) return WMTP_ERR_WORKSPACE;
+  if (batch == 0) return WMTP_OK;
+  if (target == nullptr || uniforms == nullptr || tokens_out == nullptr || count_out == nullptr)
+    return WMTP_ERR_INVALID_ARG;
+  if (num_q > 1 && draft_tokens == nullptr) return WMTP_ERR_INVALID_ARG;
+  if (!aligned(target, bytes) || !aligned(draft, bytes) ||
+      !words_ok({draft_tokens, uniforms, num_draft, temperature, tokens_out, count_out, logprobs_out}))
+    return WMTP_ERR_INVALID_ARG;
+  if (target_batch_stride < 0 || target_row_stride < 0 || draft_batch_stride < 0 || draft_row_stride < 0)
+    return WMTP_ERR_INVALID_ARG;
+  AcceptArgs a;
+  a.target = target, a.target_batch = target_batch_stride, a.target_row = target_row_stride;
+  a.draft = num_q > 1 ? draft : nullptr, a.draft_batch = draft_batch_stride, a.draft_row = draft_row_stride;
+  a.draft_tokens = draft_tokens, a.num_draft = num_draft, a.uniforms = uniforms, a.temperature = temperature;
+  a.tokens = tokens_out, a.count = count_out, a.logprobs = logprobs_out, a.status = status_word;
+  a.stats = static_cast<RowStat*>(workspace);
+  a.B = batch, a.num_q = num_q, a.V = vocab;
+  const unsigned rows = static_cast<unsigned>(batch) * (num_q + (a.draft != nullptr ? num_q - 1 : 0));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto rows_kern = dtype == WMTP_FP32   ? accept_rows_kernel<float>
+                   : dtype == WMTP_FP16 ? accept_rows_kernel<__half>
+                                        : accept_rows_kernel<__nv_bfloat16>;
+  auto kern = dtype == WMTP_FP32 ? accept_kernel<float> : dtype == WMTP_FP16 ? accept_kernel<__half>
+                                                                             : accept_kernel<__nv_bfloat16>;
+  wmtp_status s = launch_plain(true, rows_kern, dim3(rows), dim3(kRowThreads), st, a);
+  if (s != WMTP_OK) return s;
+  return launch_plain(true, kern, dim3(batch), dim3(kRowThreads), st, a);
+}
+
+}  // extern "C"

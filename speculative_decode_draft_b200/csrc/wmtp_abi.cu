@@ -15,6 +15,7 @@
 
 #include "combine.cuh"
 #include "decode_attn.cuh"
+#include "host.cuh"
 #include "ring.cuh"
 #include "verify_tc.cuh"
 #include "wmtp.h"
@@ -22,38 +23,11 @@
 namespace wmtp {
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxRows = 64;             // rows per KV head of the mma.sync kernel
 constexpr int kMaxRowsTc = 128;          // rows per KV head of the tcgen05 verify
 constexpr int kMaxGammaMax = 16;
 constexpr int kMaxVerifyWaves = 8;      // CTAs per SM in turn for the tcgen05 verify of a batch
 constexpr int kMinTilesPerSplit = 16;   // extra waves only while full-capacity splits keep this many tiles
-constexpr size_t kWsAlign = 256;
-constexpr int kMaxGridYZ = 65535;       // gridDim.y / gridDim.z limit
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// ---------------------------------------------------------------- device info
-struct DeviceInfo {
-  int sms = 0;
-};
-
-DeviceInfo g_dev[kMaxDevices];
-std::once_flag g_dev_once[kMaxDevices];
-
-wmtp_status current_device(int* dev, DeviceInfo* info) {
-  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return WMTP_ERR_CUDA;
-  const int d = *dev;
-  std::call_once(g_dev_once[d], [d]() {
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d) == cudaSuccess) g_dev[d].sms = sms;
-  });
-  if (g_dev[d].sms <= 0) return WMTP_ERR_CUDA;
-  *info = g_dev[d];
-  return WMTP_OK;
-}
 
 // ---------------------------------------------------------------- launches
 // Dynamic shared-memory opt-in of one kernel, set once per device.  Only a
@@ -78,28 +52,6 @@ wmtp_status ensure_smem_attr(SmemAttrOnce& once, Kern kern, int bytes) {
   }
   once.done[dev].store(true, std::memory_order_release);
   return WMTP_OK;
-}
-
-// A launch whose success is read from the launch call itself, never from
-// cudaGetLastError (which would also report an unrelated earlier error left
-// on this thread, after the kernel had been queued).  `programmatic`: launch
-// as a programmatic dependent of the previous work on the stream (the kernel
-// must execute griddepcontrol.wait before its first memory access).
-template <typename... Exp, typename... Act>
-wmtp_status launch_plain(bool programmatic, void (*kern)(Exp...), dim3 grid, dim3 block, cudaStream_t st,
-                         Act&&... args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = programmatic ? attr : nullptr;
-  cfg.numAttrs = programmatic ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...) == cudaSuccess ? WMTP_OK : WMTP_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -140,8 +92,6 @@ wmtp_status encode_map(CUtensorMap* m, void* base, int D, long long dim1, long l
 }
 
 // ---------------------------------------------------------------- validation
-bool supported_page(int p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
-
 wmtp_status check_params(const wmtp_params* p, int num_q) {
   if (p == nullptr) return WMTP_ERR_INVALID_ARG;
   if (p->num_heads_q <= 0 || p->num_heads_kv <= 0 || num_q <= 0) return WMTP_ERR_INVALID_ARG;
