@@ -47,22 +47,38 @@ wmtp_status current_device(int* dev, DeviceInfo* info) {
 // cudaGetLastError (which would also report an unrelated earlier error left
 // on this thread, after the kernel had been queued).  `programmatic`: launch
 // as a programmatic dependent of the previous work on the stream (the kernel
-// must execute griddepcontrol.wait before its first memory access).
+// must execute griddepcontrol.wait before its first memory access).  `cluster`:
+// CTAs per thread-block cluster, along x; it divides gridDim.x.
 template <typename... Exp, typename... Act>
-wmtp_status launch_plain(bool programmatic, void (*kern)(Exp...), dim3 grid, dim3 block, cudaStream_t st,
-                         Act&&... args) {
+wmtp_status launch_clusters(bool programmatic, void (*kern)(Exp...), dim3 grid, dim3 block, int cluster,
+                            cudaStream_t st, Act&&... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = 0;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = programmatic ? attr : nullptr;
-  cfg.numAttrs = programmatic ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (programmatic) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = n > 0 ? attr : nullptr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...) == cudaSuccess ? WMTP_OK : WMTP_ERR_CUDA;
+}
+
+template <typename... Exp, typename... Act>
+wmtp_status launch_plain(bool programmatic, void (*kern)(Exp...), dim3 grid, dim3 block, cudaStream_t st,
+                         Act&&... args) {
+  return launch_clusters(programmatic, kern, grid, block, 1, st, std::forward<Act>(args)...);
 }
 
 // ---------------------------------------------------------------- shapes

@@ -39,6 +39,16 @@ bool heads_ok(const void* p, int64_t token_stride, int64_t head_stride, int byte
          head_stride * bytes % 16 == 0;
 }
 
+// CTAs that share each of `units` pieces of work on rows of `vocab` logits: more
+// while there are too few to fill the SMs and each still has two 16-byte
+// loads for every thread.
+int row_cluster(long long units, int vocab, int bytes, int sms) {
+  int c = 1;
+  const long long vecs = static_cast<long long>(vocab) * bytes / 16;
+  while (c < kMaxCluster && units * c < 2LL * sms && vecs / (2 * c) >= 2 * kRowThreads) c *= 2;
+  return c;
+}
+
 }  // namespace
 }  // namespace wmtp
 
@@ -172,7 +182,13 @@ wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, cons
   auto kern = dtype == WMTP_FP32   ? logprob_kernel<float>
               : dtype == WMTP_FP16 ? logprob_kernel<__half>
                                    : logprob_kernel<__nv_bfloat16>;
-  return launch_plain(true, kern, dim3(rows), dim3(kRowThreads), static_cast<cudaStream_t>(stream), a);
+  int dev = 0;
+  DeviceInfo info;
+  const wmtp_status s = current_device(&dev, &info);
+  if (s != WMTP_OK) return s;
+  const int c = row_cluster(rows, vocab, bytes, info.sms);
+  return launch_clusters(true, kern, dim3(static_cast<unsigned>(rows) * c), dim3(kRowThreads), c,
+                         static_cast<cudaStream_t>(stream), a);
 }
 
 wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32_t dtype, const void* target,
@@ -214,9 +230,15 @@ wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32
                                         : accept_rows_kernel<__nv_bfloat16>;
   auto kern = dtype == WMTP_FP32 ? accept_kernel<float> : dtype == WMTP_FP16 ? accept_kernel<__half>
                                                                              : accept_kernel<__nv_bfloat16>;
-  wmtp_status s = launch_plain(true, rows_kern, dim3(rows), dim3(kRowThreads), st, a);
+  int dev = 0;
+  DeviceInfo info;
+  wmtp_status s = current_device(&dev, &info);
   if (s != WMTP_OK) return s;
-  return launch_plain(true, kern, dim3(batch), dim3(kRowThreads), st, a);
+  int c = row_cluster(rows, vocab, bytes, info.sms);
+  s = launch_clusters(true, rows_kern, dim3(rows * c), dim3(kRowThreads), c, st, a);
+  if (s != WMTP_OK) return s;
+  c = row_cluster(batch, vocab, bytes, info.sms);
+  return launch_clusters(true, kern, dim3(static_cast<unsigned>(batch) * c), dim3(kRowThreads), c, st, a);
 }
 
 }  // extern "C"
