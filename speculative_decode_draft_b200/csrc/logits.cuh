@@ -1,14 +1,12 @@
 // Rows of logits: log probabilities of given tokens with the entropy and the
 // most likely alternatives, and the acceptance of drafted tokens.
 //
-// One pass over a row keeps, per thread, the running maximum m and, with
-// t = (x - m) c and c = log2(e) / T,
-//   s = sum 2^t,   a = sum 2^t t,
-// from which lse = m / T + ln s and entropy = ln s - ln 2 * a / s.  x - m is
-// taken before the scale: that keeps the digits of large logits, and a row
-// of the type's lowest value has differences of 0.
+// One pass over a row keeps, per thread, an anchor m near the running maximum
+// and, with d = x - m and c = log2(e) / T,
+//   s = sum 2^(c d),   a = sum 2^(c d) d,
+// from which lse = m / T + ln s and entropy = ln s - a / (T s).
 //
-// A row is read once, by a cluster of up to 8 CTAs where there are few rows;
+// A row is read once, by a cluster of up to 4 CTAs where there are few rows;
 // the parts' sums meet in the shared memory of the cluster's first CTA.
 #pragma once
 
@@ -27,13 +25,17 @@ namespace wmtp {
 namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowUnroll = 4;      // 16-byte loads in flight per thread
-constexpr int kMaxCluster = 8;     // CTAs that share a row
-constexpr int kGroups = kRowThreads / 4;
+constexpr int kRowUnroll = 4;                      // 16-byte loads of a thread's batch; two batches are in flight
+constexpr int kBatch = kRowUnroll * kRowThreads;  // vecs of a CTA's batch
+constexpr int kRowCluster = 4;                     // most CTAs that share a row
+constexpr int kCells = 16;                         // of a thread, in the search for the largest logits
+constexpr int kMaxCells = 512;
 constexpr int kMaxCandidates = 1024;
+constexpr int kFinalCluster = 8;
+constexpr int kFinalThreads = 512;
+constexpr int kFinalWarps = kFinalThreads / 32;
 constexpr int kMaxTop = 64;
 
 __device__ __forceinline__ float as_float(float x) { return x; }
@@ -47,41 +49,6 @@ __device__ __forceinline__ float exp2_fast(float t) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
-
-// 16 bytes of a row as floats.
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
-template <>
-struct Vec<__half> {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-};
 
 // Two fp32 values in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -114,11 +81,101 @@ __device__ __forceinline__ float at_least(float x, float lo) {
   return r;
 }
 
-// The largest value of 16 bytes (NaN aside).
-__device__ __forceinline__ float vec_max(const float (&x)[4]) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
-__device__ __forceinline__ float vec_max(const float (&x)[8]) {
-  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-}
+// Stands for lower logits and -inf in exponents, so that none is infinite.
+constexpr float kLowest = -9.9530379158544574e29f;  // bf16 0xf149
+
+// 16 bytes of a row.  unpack: as floats.  Top, top_of: the largest value of
+// several vecs (NaN aside).  exponents: x c - A with x no lower than kLowest,
+// in pairs; NaN stays.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  using Top = float;
+  static __device__ __forceinline__ Top top_empty() { return -INFINITY; }
+  static __device__ __forceinline__ void top_add(Top& t, uint4 u) {
+    t = fmaxf(fmaxf(t, fmaxf(__uint_as_float(u.x), __uint_as_float(u.y))),
+              fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+  static __device__ __forceinline__ float top_of(Top t) { return t; }
+  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[4]) {
+    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ void exponents(uint4 u, uint64_t c, uint64_t minus_a, uint64_t (&t)[2]) {
+    float x[4];
+    unpack(u, x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      t[i] = fma2(pack2(at_least(x[2 * i], kLowest), at_least(x[2 * i + 1], kLowest)), c, minus_a);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  using Top = uint32_t;
+  static __device__ __forceinline__ Top top_empty() { return 0xff80ff80u; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ void top_add(Top& t, uint4 u) {
+    t = larger(larger(t, larger(u.x, u.y)), larger(u.z, u.w));
+  }
+  static __device__ __forceinline__ float top_of(Top t) {
+    return fmaxf(__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void exponents(uint4 u, uint64_t c, uint64_t minus_a, uint64_t (&t)[4]) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(0xf149f149u));
+      t[i] = fma2(pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), c, minus_a);
+    }
+  }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int N = 8;
+  using Top = uint32_t;
+  static __device__ __forceinline__ Top top_empty() { return 0xfc00fc00u; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ void top_add(Top& t, uint4 u) {
+    t = larger(larger(t, larger(u.x, u.y)), larger(u.z, u.w));
+  }
+  static __device__ __forceinline__ float2 both(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ float top_of(Top t) { return fmaxf(both(t).x, both(t).y); }
+  static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = both(w[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void exponents(uint4 u, uint64_t c, uint64_t minus_a, uint64_t (&t)[4]) {
+    float x[8];
+    unpack(u, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t[i] = fma2(pack2(at_least(x[2 * i], kLowest), at_least(x[2 * i + 1], kLowest)), c, minus_a);
+  }
+};
 
 // A row in aligned groups of 16 bytes ("vecs"), of which this CTA takes
 // [v0, v1), a run of columns.  The first and the last vec of a row may reach
@@ -156,19 +213,19 @@ struct Part {
   }
 };
 
-// Running sums of a part of a row.  m starts at the lowest finite value, so
-// that x - m of a masked -inf is -inf and never NaN; NaN and +inf reach s.
+// Running sums of a part of a row, relative to m.
 struct RowSum {
   float m, s, a;
 };
 
-// Moves the sums to a larger maximum.  The clamp keeps 0 * inf out: below
-// -1000 the factor is 0 in any case.
+// Moves the sums to a larger m.  Where the factor is 0 a difference may be
+// infinite; NaN in s stays.
 __device__ __forceinline__ void row_sum_raise(RowSum& r, float m, float c) {
-  const float d = fmaxf((r.m - m) * c, -1000.f);
-  const float f = exp2_fast(d);
+  const float d = r.m - m;
+  const float f = exp2_fast(d * c);
   r.a = f * (r.a + d * r.s);
   r.s *= f;
+  if (f == 0.f) r.a = r.s;
   r.m = m;
 }
 
@@ -179,69 +236,131 @@ __device__ __forceinline__ void row_sum_merge(RowSum& r, RowSum o, float c) {
   r.a += o.a;
 }
 
-// A thread's sums, and its largest logit with the first vec that holds it.
+// A thread's sums, and its largest logit with the place where it is first met:
+// one of the kRowUnroll vecs from `vec` on, as many threads apart as there are.
 struct ThreadSum {
   RowSum r;
   float best;
   int vec;
 };
 
-// Sums of this thread's share of a part.  Per logit: the widening of its 16
-// bits, a maximum, and 2^x on the special function unit; the difference, the
-// scale and the two sums take half an instruction each.
+// A thread's sums where x c may not be finite or loses the digits of x - m:
+// very large logits, lowest values of the type alone, extreme temperatures.
 template <typename T>
-__device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c) {
-  constexpr int N = Vec<T>::N;
-  ThreadSum z = {{-FLT_MAX, 0.f, 0.f}, -INFINITY, part.v0};
+__device__ __noinline__ RowSum part_sums_extreme(const Part<T>& part, float c, float best) {
+  RowSum r = {best, 0.f, 0.f};
+  for (int i = part.v0 + threadIdx.x; i < part.v1; i += kRowThreads) {
+    float x[Vec<T>::N];
+    Vec<T>::unpack(part.load(i), x);
+    for (int j = 0; j < Vec<T>::N; ++j) {
+      const float d = x[j] - best, e = exp2_fast(d * c);
+      r.s += e;
+      r.a += e == 0.f ? 0.f : e * d;
+    }
+  }
+  return r;
+}
+
+// Sums of this thread's share of a part, relative to A = m c rounded: the
+// exponent x c - A takes one fused instruction and one rounding, and 2^(m c - A),
+// the same for all of them, is put right at the end.  The anchor is raised only
+// once a logit passes it by 2^8 in weight, not at each new maximum, which some lane
+// of a warp meets nearly always.
+// cells (NULL: none): `used` cells of the thread, kRowThreads apart, the largest
+// logit of each run of 2^shift batches.
+template <typename T>
+__device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, float* cells, int used, int shift) {
+  using V = Vec<T>;
+  ThreadSum z = {{0.f, 0.f, 0.f}, -INFINITY, part.v0};
+  const float slack = 8.f / c;
   const uint64_t c2 = pack2(c, c);
-  auto step = [&](const uint4 (&u)[kRowUnroll], int i, int n) {
-    float x[kRowUnroll][N], top[kRowUnroll], most = -INFINITY;
+  uint64_t s2 = 0, a2 = 0, minus_a2 = 0;
+  float raise_at = -INFINITY;
+  auto sums = [&]() {
+    float s0, s1, a0, a1;
+    unpack2(s2, s0, s1);
+    unpack2(a2, a0, a1);
+    return make_float2(s0 + s1, a0 + a1);
+  };
+  auto step = [&](auto& u, int i) {
+    typename V::Top t = V::top_empty();
 #pragma unroll
-    for (int k = 0; k < kRowUnroll; ++k) {
-      if (k >= n) break;
-      Vec<T>::unpack(u[k], x[k]);
-      top[k] = vec_max(x[k]);
-      most = fmaxf(most, top[k]);
+    for (const uint4& v : u) V::top_add(t, v);
+    const float top = V::top_of(t);
+    if (cells != nullptr) {
+      float* cell = cells + ((i - part.v0) / kBatch >> shift) * kRowThreads;
+      *cell = fmaxf(*cell, top);
     }
-    if (most > z.best) {
-#pragma unroll
-      for (int k = kRowUnroll - 1; k >= 0; --k)
-        if (k < n && top[k] == most) z.vec = i + k * kRowThreads;
-      z.best = most;
-      if (most > z.r.m) row_sum_raise(z.r, most, c);
+    if (top > z.best) z.best = top, z.vec = i;
+    if (top > raise_at) {
+      const float2 o = sums();
+      const float by = __fmul_rn(z.r.m, c) - __fmul_rn(top, c), f = exp2_fast(by);
+      z.r.m = top;
+      raise_at = top + slack;
+      s2 = pack2(o.x == 0.f ? 0.f : f * o.x, 0.f);
+      a2 = pack2(o.x == 0.f ? 0.f : f * (o.y + by * o.x), 0.f);
+      minus_a2 = pack2(__fmul_rn(-top, c), __fmul_rn(-top, c));
     }
-    const uint64_t m2 = pack2(-z.r.m, -z.r.m);
-    uint64_t s2 = pack2(z.r.s, 0.f), a2 = pack2(z.r.a, 0.f);
 #pragma unroll
-    for (int k = 0; k < kRowUnroll; ++k) {
-      if (k >= n) break;
+    for (const uint4& v : u) {
+      uint64_t t2[V::N / 2];
+      V::exponents(v, c2, minus_a2, t2);
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
+      for (int j = 0; j < V::N / 2; ++j) {
         float t0, t1;
-        unpack2(mul2(add2(pack2(x[k][j], x[k][j + 1]), m2), c2), t0, t1);
-        t0 = at_least(t0, -1000.f), t1 = at_least(t1, -1000.f);  // 0 * -inf
-        const uint64_t e2 = pack2(exp2_fast(t0), exp2_fast(t1));
-        s2 = add2(s2, e2);
-        a2 = fma2(e2, pack2(t0, t1), a2);
+        unpack2(t2[j], t0, t1);
+        const uint64_t e = pack2(exp2_fast(t0), exp2_fast(t1));
+        s2 = add2(s2, e);
+        a2 = fma2(e, t2[j], a2);
       }
     }
-    float lo, hi;
-    unpack2(s2, lo, hi);
-    z.r.s = lo + hi;
-    unpack2(a2, lo, hi);
-    z.r.a = lo + hi;
   };
   int i = part.v0 + threadIdx.x;
-  for (; i + (kRowUnroll - 1) * kRowThreads < part.v1; i += kRowUnroll * kRowThreads) {
-    uint4 u[kRowUnroll];
-#pragma unroll
-    for (int k = 0; k < kRowUnroll; ++k) u[k] = part.load(i + k * kRowThreads);
-    step(u, i, kRowUnroll);
+  auto single = [&]() {
+    uint4 u[1] = {part.load(i)};
+    step(u, i);
+    i += kRowThreads;
+  };
+  if (cells != nullptr) {
+    cells += threadIdx.x;
+    for (int k = 0; k < used; ++k) cells[k * kRowThreads] = -INFINITY;
   }
-  for (; i < part.v1; i += kRowThreads) {
-    uint4 u[kRowUnroll];
-    u[0] = part.load(i);
-    step(u, i, 1);
+  if (part.col(i) < 0)  // the row's first vec is cut: the thread's first batch one by one
+    for (int k = 0; k < kRowUnroll && i < part.v1; ++k) single();
+  // whole vecs in batches, the next batch's loads in flight while one is summed
+  const int whole = part.v1 - (part.col(part.v1) > part.V ? 1 : 0) - (kRowUnroll - 1) * kRowThreads;
+  if (i < whole) {
+    const uint4* v = reinterpret_cast<const uint4*>(part.p + part.col(i));
+    uint4 u0[kRowUnroll], u1[kRowUnroll];
+    auto fetch = [&](uint4 (&u)[kRowUnroll]) {
+#pragma unroll
+      for (int k = 0; k < kRowUnroll; ++k) u[k] = __ldg(v + k * kRowThreads);
+      v += kBatch;
+    };
+    fetch(u0);
+    while (true) {
+      const bool one = i + kBatch < whole, two = i + 2 * kBatch < whole;
+      if (one) fetch(u1);
+      step(u0, i);
+      i += kBatch;
+      if (!one) break;
+      if (two) fetch(u0);
+      step(u1, i);
+      i += kBatch;
+      if (!two) break;
+    }
+  }
+  while (i < part.v1) single();
+  const float2 o = sums();
+  z.r.s = o.x, z.r.a = o.y;
+  if (z.best == -INFINITY) {  // masked: no weight, but NaN stays
+    z.r.m = -FLT_MAX;
+  } else if (fabsf(z.r.m) < 1e29f && fabsf(z.r.m * c) < 1e6f && c > 1e-20f && c < 1e7f) {
+    const float low = fmaf(z.r.m, c, -__fmul_rn(z.r.m, c)), f = exp2f(-low);
+    z.r.s = f * o.x;
+    z.r.a = f * (o.y - low * o.x) / c;
+  } else {
+    z.r = part_sums_extreme<T>(part, c, z.best);
   }
   return z;
 }
@@ -274,15 +393,15 @@ __device__ __forceinline__ RowSum block_sums(RowSum r, float c, RowSum* s_part) 
   if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = r;
   __syncthreads();
   if (threadIdx.x < 32) {
-    r = s_part[threadIdx.x & (kRowWarps - 1)];
-    halve(kRowWarps / 2);
+    r = s_part[threadIdx.x & (kRowThreads / 32 - 1)];
+    halve(kRowThreads / 64);
   }
   return r;
 }
 
 // The largest key of the part below `bound`, on every thread.  0: none above -inf.
 template <typename T>
-__device__ uint64_t part_best(const Part<T>& part, uint64_t bound, uint64_t* s_best) {
+__device__ __noinline__ uint64_t part_best(const Part<T>& part, uint64_t bound, uint64_t* s_best) {
   uint64_t best = 0;
   for (int i = part.v0 + threadIdx.x; i < part.v1; i += kRowThreads) {
     float x[Vec<T>::N];
@@ -299,63 +418,70 @@ __device__ uint64_t part_best(const Part<T>& part, uint64_t bound, uint64_t* s_b
   if ((threadIdx.x & 31) == 0) s_best[threadIdx.x >> 5] = best;
   __syncthreads();
   best = s_best[0];
-  for (int w = 1; w < kRowWarps; ++w) best = max_key(best, s_best[w]);
+  for (int w = 1; w < kRowThreads / 32; ++w) best = max_key(best, s_best[w]);
   return best;
 }
 
 struct TopShared {
-  uint64_t keys[kGroups];
+  float cells[kCells * kRowThreads];
+  uint64_t keys[kRowThreads / 2];
   uint64_t cand[kMaxCandidates];
   uint64_t warp_best[kRowWarps];
   uint64_t bound;
-  int group[kMaxTop];
-  int count;
+  int cell[kMaxCells];
+  int listed, count;
 };
 
-// The part's `top_k` largest keys, in order, to out[0 .. top_k).
+// The part's `top_k` largest keys, in order, to out[0 .. top_k), 0 behind the
+// last one.  Returns how many there are.
 //
-// Four threads are a group, and a key at or below its best logit's is known
-// from the pass over the row.  The top_k-th largest of the groups' keys bounds
-// the part's top_k-th logit from below, and what lies above it is in the
-// top_k groups that reach it: only their vecs are read again (from L2), and
-// the few logits above the bound sorted by counting.  Should one group hold so
-// many of them that the list overflows, the keys are taken one pass each.
+// The pass over the row leaves each thread its best logit and the best of each of its
+// cells; the keys lie between those of the first and the last column that they may
+// stand in.  The top_k-th largest of the lower bounds of groups of threads
+// bounds the part's top_k-th key from below, and what lies above it is in the cells
+// whose upper bound reaches it, about top_k of them: only these are read again
+// (from L2), and the few keys above the bound sorted by counting.  Should a list
+// overflow (a great many equal logits), the keys are taken one pass each.
 template <typename T>
-__device__ void part_top(const Part<T>& part, const ThreadSum& z, int top_k, TopShared& sh, uint64_t* out) {
+__device__ __forceinline__ int part_top(const Part<T>& part, const ThreadSum& z, int used, int shift, int top_k,
+                                        TopShared& sh, uint64_t* out) {
   constexpr int N = Vec<T>::N;
   const int tid = threadIdx.x;
-  // the vec's last column: at or below the best logit's own key
-  uint64_t key = z.best > -INFINITY ? logit_key(z.best, part.col(z.vec) + N - 1) : 0;
-#pragma unroll
-  for (int o = 2; o > 0; o >>= 1) key = max_key(key, __shfl_xor_sync(0xffffffffu, key, o));
-  if ((tid & 3) == 0) sh.keys[tid >> 2] = key;
-  if (tid == 0) sh.count = 0, sh.bound = 0;
-  for (int i = tid; i < top_k; i += kRowThreads) sh.group[i] = -1, out[i] = 0;
+  uint64_t least = 0;
+  if (z.best > -INFINITY) least = logit_key(z.best, part.col(z.vec + (kRowUnroll - 1) * kRowThreads) + N - 1);
+  const int lanes = top_k <= 16 ? 8 : top_k <= 32 ? 4 : 2;  // of a group: twice top_k groups bound well
+  for (int o = lanes / 2; o > 0; o >>= 1) least = max_key(least, __shfl_xor_sync(0xffffffffu, least, o));
+  if (tid % lanes == 0) sh.keys[tid / lanes] = least;
+  if (tid == 0) sh.listed = sh.count = 0, sh.bound = 0;
+  for (int i = tid; i < top_k; i += kRowThreads) out[i] = 0;
   __syncthreads();
-  // each thread ranks its group's key among a quarter of the keys
+  // each thread ranks its group's key among its share of the keys
   int rank = 0;
-#pragma unroll 8
-  for (int i = tid & 3; i < kGroups; i += 4) rank += sh.keys[i] > key;
-  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-  if ((tid & 3) == 0 && key != 0 && rank < top_k) {
-    sh.group[rank] = tid >> 2;
-    if (rank == top_k - 1) sh.bound = key;
-  }
+#pragma unroll 4
+  for (int i = tid % lanes; i < kRowThreads / lanes; i += lanes) rank += sh.keys[i] > least;
+  for (int o = lanes / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (rank == top_k - 1 && tid % lanes == 0) sh.bound = least;  // 0 where there are fewer: every cell
   __syncthreads();
   const uint64_t bound = sh.bound;
-  const float least = bound != 0 ? key_logit(bound) : -FLT_MAX;
-  const int rounds = (part.v1 - part.v0 + kRowThreads - 1) / kRowThreads;
-  for (int i = tid; i < top_k * rounds * 4; i += kRowThreads) {
-    const int g = sh.group[i / (rounds * 4)];
-    const int v = part.v0 + (i / 4 % rounds) * kRowThreads + g * 4 + (i & 3);
-    if (g < 0 || v >= part.v1) continue;
+  const float lowest = bound != 0 ? key_logit(bound) : -FLT_MAX;
+  auto first_vec = [&](int cell) { return part.v0 + (cell / kRowThreads << shift) * kBatch + cell % kRowThreads; };
+  if (z.best >= lowest)
+    for (int i = tid; i < used * kRowThreads; i += kRowThreads) {
+      const float x = sh.cells[i];
+      if (!(x >= lowest) || logit_key(x, max(part.col(first_vec(i)), 0)) < bound) continue;
+      const int at = atomicAdd(&sh.listed, 1);
+      if (at < kMaxCells) sh.cell[at] = i;
+    }
+  __syncthreads();
+  const int listed = sh.listed, vecs = kRowUnroll << shift;
+  for (int i = tid; i < min(listed, kMaxCells) << (shift + 2); i += kRowThreads) {
+    const int v = first_vec(sh.cell[i >> (shift + 2)]) + (i & (vecs - 1)) * kRowThreads;
+    if (v >= part.v1) continue;
     float x[N];
     Vec<T>::unpack(part.load(v), x);
-    if (!(vec_max(x) >= least)) continue;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (!(x[j] >= least)) continue;
+      if (!(x[j] >= lowest)) continue;
       const uint64_t k = logit_key(x[j], part.col(v) + j);
       if (k < bound) continue;
       const int at = atomicAdd(&sh.count, 1);
@@ -363,22 +489,25 @@ __device__ void part_top(const Part<T>& part, const ThreadSum& z, int top_k, Top
     }
   }
   __syncthreads();
-  const int n = sh.count;
-  if (n <= kMaxCandidates) {
+  int n = sh.count;
+  if (listed <= kMaxCells && n <= kMaxCandidates) {
     for (int i = tid; i < n; i += kRowThreads) {
       const uint64_t k = sh.cand[i];
       int r = 0;
       for (int j = 0; j < n; ++j) r += sh.cand[j] > k;
       if (r < top_k) out[r] = k;
     }
+    n = min(n, top_k);
   } else {
     uint64_t below = ~0ull;
-    for (int i = 0; i < top_k && below != 0; ++i) {
-      below = part_best(part, below, sh.warp_best);
-      if (tid == 0) out[i] = below;
+    for (n = 0; n < top_k; ++n) {
+      below = part_best<T>(part, below, sh.warp_best);
+      if (below == 0) break;
+      if (tid == 0) out[n] = below;
     }
   }
   __syncthreads();
+  return n;
 }
 
 // A row's temperature: 1 / T, or NaN for one that is no temperature.
@@ -402,92 +531,100 @@ struct LogprobArgs {
   int V, num_tokens, top_k;
 };
 
+// What a CTA knows of its part of a row.
+struct PartSum {
+  RowSum r;
+  int n;          // keys in its list
+  uint64_t best;  // the largest key
+};
+
 // One cluster per row; its first CTA joins the parts and writes the results.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) logprob_kernel(LogprobArgs a) {
-  __shared__ RowSum s_part[kRowWarps];
-  __shared__ RowSum s_sums[kMaxCluster];
-  __shared__ uint64_t s_top[kMaxCluster * kMaxTop];
+__global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) logprob_kernel(LogprobArgs a) {
+  __shared__ RowSum s_part[kRowThreads / 32];
+  __shared__ PartSum s_sums[kRowCluster];
+  __shared__ uint64_t s_top[kRowCluster * kMaxTop];
   __shared__ uint64_t s_mine[kMaxTop];
   __shared__ TopShared s_sel;
   const cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), rank = cluster.block_rank();
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const int r = blockIdx.x / parts, tid = threadIdx.x;
   const T* p = static_cast<const T*>(a.logits) + r * a.row_stride;
-  const Part<T> part(p, a.V, rank, parts);
   const float inv_t = inverse_temperature(a.temperature, r), c = inv_t * kLog2e;
-  const ThreadSum z = part_sums(part, c);
+  // the given tokens' logits, while the row is read
+  const int32_t* ids = a.tokens + static_cast<size_t>(r) * a.num_tokens;
+  int id = -1;
+  float x_id = 0.f;
+  if (rank == 0 && tid < a.num_tokens) {
+    id = ids[tid];
+    if (id >= 0 && id < a.V) x_id = as_float(p[id]);
+  }
+  const Part<T> part(p, a.V, rank, parts);
+  const int batches = (part.v1 - part.v0 + kBatch - 1) / kBatch;
+  int shift = 0;
+  while ((batches - 1) >> shift >= kCells) ++shift;
+  const int used = (batches + (1 << shift) - 1) >> shift;
+  const ThreadSum z = part_sums<T>(part, c, a.top_k > 0 ? s_sel.cells : nullptr, used, shift);
   RowSum sum = block_sums(z.r, c, s_part);
-  if (a.top_k > 0) part_top(part, z, a.top_k, s_sel, parts > 1 ? s_mine : s_top);
-  // the first CTA has started by now, so its shared memory may be written
+  const int mine = a.top_k > 0 ? part_top<T>(part, z, used, shift, a.top_k, s_sel, parts > 1 ? s_mine : s_top) : 0;
   if (parts > 1) {
+    // the first CTA has started by now, so its shared memory may be written
     asm volatile("barrier.cluster.wait;" ::: "memory");
-    if (tid == 0) cluster.map_shared_rank(s_sums, 0)[rank] = sum;
+    if (tid == 0) cluster.map_shared_rank(s_sums, 0)[rank] = {sum, mine, 0};
     uint64_t* top = cluster.map_shared_rank(s_top, 0) + rank * kMaxTop;
     for (int i = tid; i < a.top_k; i += kRowThreads) top[i] = s_mine[i];
     cluster.sync();
     if (rank != 0) return;
   } else {
-    if (tid == 0) s_sums[0] = sum;
+    if (tid == 0) s_sums[0] = {sum, mine, 0};
     __syncthreads();
   }
-  sum = s_sums[0];
-  for (int i = 1; i < parts; ++i) row_sum_merge(sum, s_sums[i], c);
+  sum = s_sums[0].r;
+  int have = s_sums[0].n;
+  for (int i = 1; i < parts; ++i) {
+    row_sum_merge(sum, s_sums[i].r, c);
+    have += s_sums[i].n;
+  }
   const bool bad = row_bad(sum, inv_t), none = sum.s == 0.f;
   const float ln_s = bad ? NAN : logf(sum.s);
   if (bad && tid == 0) set_status(a.status, kDevLogits);
   for (int j = tid; j < a.num_tokens; j += kRowThreads) {
-    const int id = a.tokens[static_cast<size_t>(r) * a.num_tokens + j];
+    if (j != tid) id = ids[j];
     const bool in = id >= 0 && id < a.V;
+    if (j != tid && in) x_id = as_float(p[id]);
     if (!in && id != -1) set_status(a.status, kDevTokenOob);
     a.logprobs[static_cast<size_t>(r) * a.num_tokens + j] =
-        bad ? NAN : (none || !in) ? -INFINITY : (as_float(p[id]) - sum.m) * inv_t - ln_s;
+        bad ? NAN : (none || !in) ? -INFINITY : (x_id - sum.m) * inv_t - ln_s;
   }
   if (tid == 0) {
     if (a.lse != nullptr) a.lse[r] = bad ? NAN : none ? -INFINITY : sum.m * inv_t + ln_s;
-    if (a.entropy != nullptr) a.entropy[r] = bad ? NAN : none ? 0.f : ln_s - kLn2 * sum.a / sum.s;
+    if (a.entropy != nullptr) a.entropy[r] = bad ? NAN : none ? 0.f : ln_s - inv_t * sum.a / sum.s;
   }
   // every part's list is in order: a key's place is its own in its list plus,
   // in each other list, the number of keys above it
   const size_t o = static_cast<size_t>(r) * a.top_k;
-  for (int i = tid; i < parts * a.top_k; i += kRowThreads) {
-    const int l = i / a.top_k, at = i % a.top_k;
-    const uint64_t key = s_top[l * kMaxTop + at];
+  for (int i = tid; i < kMaxTop * parts && !bad; i += kRowThreads) {
+    const int l = i / kMaxTop, at = i % kMaxTop;
+    if (at >= s_sums[l].n) continue;
+    const uint64_t key = s_top[i];
     int place = at;
-    if (key == 0 || bad) continue;
-    for (int other = 0; other < parts; ++other) {
-      if (other == l) continue;
-      int lo = 0, hi = a.top_k;  // the first key below this one
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (s_top[other * kMaxTop + mid] > key)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      place += lo;
+#pragma unroll
+    for (int other = 0; other < kRowCluster; ++other) {
+      if (other >= parts || other == l) continue;
+      int above = 0;
+#pragma unroll
+      for (int step = kMaxTop; step > 0; step >>= 1)
+        if (above + step <= s_sums[other].n && s_top[other * kMaxTop + above + step - 1] > key) above += step;
+      place += above;
     }
     if (place >= a.top_k) continue;
     a.top_ids[o + place] = key_col(key);
     a.top_logprobs[o + place] = (key_logit(key) - sum.m) * inv_t - ln_s;
   }
-  if (a.top_k == 0) return;
-  int have = 0;  // places without a token
-  for (int l = 0; l < parts; ++l) {
-    int lo = 0, hi = a.top_k;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s_top[l * kMaxTop + mid] != 0)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    have += lo;
-  }
-  for (int i = (bad ? 0 : have) + tid; i < a.top_k; i += kRowThreads) {
+  for (int i = (bad ? 0 : have) + tid; i < a.top_k; i += kRowThreads) {  // places without a token
     a.top_ids[o + i] = -1;
     a.top_logprobs[o + i] = bad ? NAN : -INFINITY;
   }
@@ -499,6 +636,13 @@ struct alignas(16) RowStat {
   float m, s;
   int32_t best;  // lowest column with the largest logit
   int32_t bad;   // defines no distribution
+};
+
+// What is left to do for a sequence: the draw of its token `k`.
+struct Draw {
+  int32_t k;  // -1: nothing
+  int32_t drafted, minus;
+  float pm, ps, qm, qs, u;
 };
 
 struct AcceptArgs {
@@ -518,13 +662,13 @@ __device__ __forceinline__ float accept_temperature(const AcceptArgs& a, int b) 
 
 // One cluster per row of the target and of the draft.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) accept_rows_kernel(AcceptArgs a) {
-  __shared__ RowSum s_part[kRowWarps];
-  __shared__ RowSum s_sums[kMaxCluster];
-  __shared__ uint64_t s_best[kMaxCluster];
-  __shared__ uint64_t s_warp[kRowWarps];
+__global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) accept_rows_kernel(AcceptArgs a) {
+  __shared__ RowSum s_part[kRowThreads / 32];
+  __shared__ PartSum s_sums[kRowCluster];
+  __shared__ uint64_t s_warp[kRowThreads / 32];
   const cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), rank = cluster.block_rank(), tid = threadIdx.x;
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int at = blockIdx.x / parts, rows_t = a.B * a.num_q;
@@ -535,87 +679,95 @@ __global__ void __launch_bounds__(kRowThreads) accept_rows_kernel(AcceptArgs a) 
   const float temp = accept_temperature(a, b);
   const bool greedy = temp == 0.f;
   const int nd = a.num_draft != nullptr ? a.num_draft[b] : a.num_q - 1;
-  if (target ? i > nd : (i >= nd || greedy)) return;  // never looked at
-  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-  const T* p = target ? static_cast<const T*>(a.target) + b * a.target_batch + i * a.target_row
-                      : static_cast<const T*>(a.draft) + b * a.draft_batch + i * a.draft_row;
-  const Part<T> part(p, a.V, rank, parts);
-  const float inv_t = greedy ? 1.f : (temp > 0.f && temp < INFINITY) ? 1.f / temp : NAN;
-  const float c = inv_t * kLog2e;
-  const ThreadSum z = part_sums(part, c);
-  RowSum sum = block_sums(z.r, c, s_part);
-  uint64_t best = 0;
-  if (greedy) {  // the lowest column with the largest logit
-    if (z.best > -INFINITY) {
-      float x[Vec<T>::N];
-      Vec<T>::unpack(part.load(z.vec), x);
+  const bool idle = target ? i > nd : (i >= nd || greedy);  // never looked at
+  if (!idle) {
+    const T* p = target ? static_cast<const T*>(a.target) + b * a.target_batch + i * a.target_row
+                        : static_cast<const T*>(a.draft) + b * a.draft_batch + i * a.draft_row;
+    const Part<T> part(p, a.V, rank, parts);
+    const float inv_t = greedy ? 1.f : (temp > 0.f && temp < INFINITY) ? 1.f / temp : NAN;
+    const float c = inv_t * kLog2e;
+    const ThreadSum z = part_sums<T>(part, c, nullptr, 0, 0);
+    RowSum sum = block_sums(z.r, c, s_part);
+    uint64_t best = 0;
+    if (greedy) {  // the lowest column with the largest logit
+      if (z.best > -INFINITY) {
 #pragma unroll
-      for (int j = Vec<T>::N - 1; j >= 0; --j)
-        if (x[j] == z.best) best = logit_key(x[j], part.col(z.vec) + j);
+        for (int k = kRowUnroll - 1; k >= 0; --k) {
+          const int v = z.vec + k * kRowThreads;
+          if (v >= part.v1) continue;
+          float x[Vec<T>::N];
+          Vec<T>::unpack(part.load(v), x);
+#pragma unroll
+          for (int j = Vec<T>::N - 1; j >= 0; --j)
+            if (x[j] == z.best) best = logit_key(x[j], part.col(v) + j);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
+      if ((tid & 31) == 0) s_warp[tid >> 5] = best;
+      __syncthreads();
+      for (int w = 0; w < kRowThreads / 32; ++w) best = max_key(best, s_warp[w]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if ((tid & 31) == 0) s_warp[tid >> 5] = best;
-    __syncthreads();
-    for (int w = 0; w < kRowWarps; ++w) best = max_key(best, s_warp[w]);
-  }
-  if (parts > 1) {
+    if (parts > 1) {
+      asm volatile("barrier.cluster.wait;" ::: "memory");
+      if (tid == 0) cluster.map_shared_rank(s_sums, 0)[rank] = {sum, 0, best};
+      cluster.sync();
+    } else if (tid == 0) {
+      s_sums[0] = {sum, 0, best};
+    }
+    if (rank == 0 && tid == 0) {
+      sum = s_sums[0].r;
+      for (int k = 1; k < parts; ++k) {
+        row_sum_merge(sum, s_sums[k].r, c);
+        best = max_key(best, s_sums[k].best);
+      }
+      a.stats[at] = {sum.m, sum.s, best != 0 ? key_col(best) : -1, row_bad(sum, inv_t) || sum.s == 0.f};
+    }
+  } else if (parts > 1) {
     asm volatile("barrier.cluster.wait;" ::: "memory");
-    if (tid == 0) {
-      cluster.map_shared_rank(s_sums, 0)[rank] = sum;
-      cluster.map_shared_rank(s_best, 0)[rank] = best;
-    }
-    cluster.sync();
-  } else if (tid == 0) {
-    s_sums[0] = sum, s_best[0] = best;
   }
-  if (rank != 0 || tid != 0) return;
-  sum = s_sums[0];
-  for (int k = 1; k < parts; ++k) {
-    row_sum_merge(sum, s_sums[k], c);
-    best = max_key(best, s_best[k]);
-  }
-  a.stats[at] = {sum.m, sum.s, best != 0 ? key_col(best) : -1, row_bad(sum, inv_t) || sum.s == 0.f};
 }
 
 // exp in 64 bits, for weights: 2^(u / 32) with u = k + r, |r| <= 1/2, is
 // 2^(k div 32) * 2^((k mod 32) / 32) * (1 + z + z^2/2 + z^3/6 + z^4/24),
 // z = r ln2 / 32; the Taylor series' next term is below 1.3e-12.  The 32
-// factors 2^(j / 32) are held by a warp's lanes.  All lanes take part.
+// factors 2^(j / 32) are held by a warp's lanes.  All lanes take part.  u is
+// raised to -32000 (the comparison of the upper words as unsigned numbers
+// orders negative ones by size): 2^-1000 stands for 0, and sums below
+// kNoWeight are taken for it.
+constexpr unsigned kLeast = 0xc0df4000u;  // upper word of -32000.0
+constexpr double kNoWeight = 1e-250;
 __device__ __forceinline__ double lane_factor() { return exp2((threadIdx.x & 31) / 32.0); }
 __device__ __forceinline__ double exp_weight(double u, double factor) {
   constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: rounds to whole numbers
   constexpr double c1 = 0.69314718055994530942 / 32, c2 = c1 * c1 / 2, c3 = c1 * c1 * c1 / 6, c4 = c1 * c1 * c1 * c1 / 24;
-  const bool none = !(u > -32000.0);  // below 2^-1000: 0
-  u = none ? 0.0 : u;
+  u = __hiloint2double(min(static_cast<unsigned>(__double2hiint(u)), kLeast), __double2loint(u));
   const double kd = u + kMagic;
   const int k = __double2loint(kd);
   const double r = u - (kd - kMagic);
   const double z = r * fma(r, fma(r, fma(r, c4, c3), c2), c1);
   const double f = __shfl_sync(0xffffffffu, factor, k & 31);
   const double e = fma(f, z, f);
-  return none ? 0.0 : __hiloint2double(__double2hiint(e) + (k >> 5) * (1 << 20), __double2loint(e));
+  return __hiloint2double(__double2hiint(e) + (k >> 5) * (1 << 20), __double2loint(e));
 }
 
-// The weights of the token that follows: p, or what p has above q.  In 64
-// bits: a draw takes the token in which the cumulated weight passes u, and with
-// V tokens a relative error e of that sum moves the border over a token with
-// probability V e (1e-2 at V = 131072 and the 1e-7 of fp32).
+// The weights of the token that follows: p, or what p has above q (both not
+// normalised: p_i - r q_i with r = sum p / sum q).  In 64 bits: a draw takes the
+// token in which the cumulated weight passes u, and with V tokens a relative
+// error e of that sum moves the border over a token with probability V e (1e-2 at
+// V = 131072 and the 1e-7 of fp32).
 template <typename T>
 struct FinalWeights {
-  const T *p, *q;  // q NULL: none, or all of it on `drafted`
-  double pm, qm, scale;     // 32 log2(e) / T
-  double p_part, q_part;    // 1 / sum
-  double factor;
+  const T *p, *q;  // q NULL: nothing to take away, or all of it on `drafted`
+  double pm, qm, scale;  // 32 log2(e) / T
+  double r, factor;
   int drafted;  // -1: no draft to take away
-  bool residual;
   __device__ __forceinline__ double pe(float x) const { return exp_weight((x - pm) * scale, factor); }
   __device__ __forceinline__ double qe(float x) const { return exp_weight((x - qm) * scale, factor); }
   __device__ __forceinline__ double operator()(float xp, float xq, int col) const {
     const double e = pe(xp);
-    if (!residual) return e;
     if (q == nullptr) return col == drafted ? 0.0 : e;
-    return fmax(e * p_part - qe(xq) * q_part, 0.0);
+    return fmax(e - r * qe(xq), 0.0);
   }
 };
 
@@ -630,222 +782,244 @@ constexpr int kFinalUnroll = 8;
 // f(logit of p, logit of q, column) of the columns [c0, c1), a warp's; columns
 // behind c1 are masked.  32 columns at a time, kFinalUnroll loads in flight.
 template <typename T, typename F>
-__device__ __forceinline__ void warp_columns(const FinalWeights<T>& w, bool with_q, int c0, int c1, F f) {
+__device__ __forceinline__ void warp_columns(const T* p, const T* q, int c0, int c1, F f) {
   const int lane = threadIdx.x & 31;
-  for (int base = c0; base < c1; base += 32 * kFinalUnroll) {
+  int base = c0;
+  for (; base + 32 * kFinalUnroll <= c1; base += 32 * kFinalUnroll) {
     float xp[kFinalUnroll], xq[kFinalUnroll];
 #pragma unroll
     for (int k = 0; k < kFinalUnroll; ++k) {
-      const int c = base + 32 * k + lane;
-      xp[k] = c < c1 ? as_float(w.p[c]) : -INFINITY;
-      xq[k] = with_q && c < c1 ? as_float(w.q[c]) : -INFINITY;
+      xp[k] = as_float(p[base + lane + 32 * k]);
+      xq[k] = q != nullptr ? as_float(q[base + lane + 32 * k]) : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < kFinalUnroll; ++k)
-      if (base + 32 * k < c1) f(xp[k], xq[k], base + 32 * k + lane);
+    for (int k = 0; k < kFinalUnroll; ++k) f(xp[k], xq[k], base + lane + 32 * k);
+  }
+  for (; base < c1; base += 32) {
+    const int c = base + lane;
+    f(c < c1 ? as_float(p[c]) : -INFINITY, q != nullptr && c < c1 ? as_float(q[c]) : -INFINITY, c);
   }
 }
 
 template <typename T>
 __device__ __forceinline__ double warp_weight(const FinalWeights<T>& w, int c0, int c1) {
   double sum = 0.0;
-  warp_columns(w, w.residual && w.q != nullptr, c0, c1, [&](float xp, float xq, int col) { sum += w(xp, xq, col); });
+  warp_columns(w.p, w.q, c0, c1, [&](float xp, float xq, int col) { sum += w(xp, xq, col); });
   return warp_total(sum);
 }
 
-// The first of n sums (at most 128, in shared memory) above 0 at which the
-// running total passes `want`, and the total before it; where rounding lets none
-// pass, the last one above 0.  *all: the total.  The same on every lane.
-__device__ __forceinline__ int warp_pick(const double* sums, int n, double want, double* before, double* all) {
-  const int lane = threadIdx.x & 31;
-  double v[4], mine = 0.0;
+// A warp's running total over v, lane by lane; *all: the total.
+template <int K>
+struct Running {
+  double v[K], before, all;  // before this lane's first
+  __device__ __forceinline__ void scan() {
+    double mine = 0.0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = 4 * lane + i < n ? sums[4 * lane + i] : 0.0;
-    mine += v[i];
-  }
-  double scan = mine;
+    for (int i = 0; i < K; ++i) mine += v[i];
+    double s = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const double u = __shfl_up_sync(0xffffffffu, s, o);
+      if ((threadIdx.x & 31) >= o) s += u;
+    }
+    all = __shfl_sync(0xffffffffu, s, 31);
+    before = s - mine;
   }
-  *all = __shfl_sync(0xffffffffu, scan, 31);
-  double b = __shfl_up_sync(0xffffffffu, scan, 1);
-  if (lane == 0) b = 0.0;
-  int at = -1, last = -1;
-  double at_before = 0.0, last_before = 0.0;
+  // The first entry with a weight at which the running total passes `want`, and the
+  // total before it; where rounding lets none pass, the last one with a weight.
+  __device__ __forceinline__ int pick(double want, double* skipped) const {
+    int at = -1, last = -1;
+    double b = before, at_before = 0.0, last_before = 0.0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (at < 0 && v[i] > 0.0 && b + v[i] > want) at = 4 * lane + i, at_before = b;
-    if (v[i] > 0.0) last = 4 * lane + i, last_before = b;
-    b += v[i];
+    for (int i = 0; i < K; ++i) {
+      if (v[i] > kNoWeight) {
+        last = i, last_before = b;
+        if (at < 0 && b + v[i] > want) at = i, at_before = b;
+      }
+      b += v[i];
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
+    const int from = hit != 0 ? __ffs(hit) - 1 : any != 0 ? 31 - __clz(any) : 0;
+    *skipped = __shfl_sync(0xffffffffu, hit != 0 ? at_before : last_before, from);
+    return from * K + max(__shfl_sync(0xffffffffu, hit != 0 ? at : last, from), 0);
   }
-  const unsigned hit = __ballot_sync(0xffffffffu, at >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
-  if (hit != 0) {
-    *before = __shfl_sync(0xffffffffu, at_before, __ffs(hit) - 1);
-    return __shfl_sync(0xffffffffu, at, __ffs(hit) - 1);
-  }
-  const int from = any != 0 ? 31 - __clz(any) : 0;
-  *before = __shfl_sync(0xffffffffu, last_before, from);
-  return __shfl_sync(0xffffffffu, last, from);
-}
+};
 
 // One cluster per sequence.
+//
+// The weights' sums take one pass: p_i - r q_i is above 0 for the same i whether
+// r is exact or from the rows' fp32 sums, but for those within 1e-7 of 0; so the sums
+// of p, of q, and of both over the i with a weight give the exact r and with it
+// each run's sum.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) accept_kernel(AcceptArgs a) {
-  constexpr int kMost = kMaxCluster * kRowWarps;
-  __shared__ double s_p[kMost], s_q[kMost], s_w[2][kMost], s_sub[kRowWarps];
+__global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) {
+  constexpr int kMost = kFinalCluster * kFinalWarps, kPer = kMost / 32;
+  __shared__ double s_sum[4][kMost];  // of each warp's run: p, q, p and q where there is a weight
+  __shared__ double s_sub[kFinalWarps];
+  __shared__ Draw s_draw;
   const cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), rank = cluster.block_rank();
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  const double factor = lane_factor();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x / parts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_q;
   const float temp = accept_temperature(a, b);
-  const bool greedy = temp == 0.f;
-  const float inv_t = greedy ? 1.f : 1.f / temp;
-  const int nd = a.num_draft != nullptr ? a.num_draft[b] : n - 1;
   const T* target = static_cast<const T*>(a.target) + b * a.target_batch;
   const T* draft = a.draft != nullptr ? static_cast<const T*>(a.draft) + b * a.draft_batch : nullptr;
-  const RowStat* ts = a.stats + static_cast<size_t>(b) * n;
-  const RowStat* ds = a.stats + static_cast<size_t>(a.B) * n + static_cast<size_t>(b) * (n - 1);
-  const int32_t* d = a.draft_tokens + static_cast<size_t>(b) * (n - 1);
-  int32_t* tokens = a.tokens + static_cast<size_t>(b) * n;
-  float* lps = a.logprobs != nullptr ? a.logprobs + static_cast<size_t>(b) * n : nullptr;
-  const bool writes = rank == 0 && warp == 0;
-  if (nd < 0 || nd > n - 1) {
-    if (writes && lane < n) {
-      tokens[lane] = -1;
-      if (lps != nullptr) lps[lane] = 0.f;
+  if (warp == 0) {
+    const int nd = a.num_draft != nullptr ? a.num_draft[b] : n - 1;
+    // a lane for each row; those behind num_draft hold nothing, and are not looked at
+    RowStat ts = RowStat(), ds = RowStat();
+    float u = 0.f;
+    int id = -1;
+    if (lane < n) {
+      ts = a.stats[static_cast<size_t>(b) * n + lane];
+      u = a.uniforms[static_cast<size_t>(b) * n + lane];
     }
-    if (writes && lane == 0) {
-      set_status(a.status, kDevLenOob);
-      a.count[b] = 0;
+    if (lane < n - 1) {
+      if (draft != nullptr) ds = a.stats[static_cast<size_t>(a.B) * n + static_cast<size_t>(b) * (n - 1) + lane];
+      id = a.draft_tokens[static_cast<size_t>(b) * (n - 1) + lane];
     }
-    return;
-  }
-  // every warp takes the same decisions, a lane for each drafted token
-  int id = -1;
-  float lp = 0.f;
-  bool ok = false, row_is_bad = false, in = true;
-  if (lane <= nd) {
-    const RowStat t = ts[lane];
-    row_is_bad = t.bad;
-    if (lane < nd) {
-      id = d[lane];
-      in = id >= 0 && id < a.V;
-      const bool with_q = !greedy && draft != nullptr;
-      const RowStat q = with_q ? ds[lane] : RowStat();
-      if (with_q && q.bad) row_is_bad = true;
-      if (in && !row_is_bad) {
-        const float y = (as_float(target[lane * a.target_row + id]) - t.m) * inv_t;
-        lp = y - logf(t.s);
-        const float qd = with_q ? expf((as_float(draft[lane * a.draft_row + id]) - q.m) * inv_t) / q.s : 1.f;
-        ok = greedy ? id == t.best : a.uniforms[static_cast<size_t>(b) * n + lane] * qd < expf(y) / t.s;
+    int32_t* tokens = a.tokens + static_cast<size_t>(b) * n;
+    float* lps = a.logprobs != nullptr ? a.logprobs + static_cast<size_t>(b) * n : nullptr;
+    if (nd < 0 || nd > n - 1) {
+      if (rank == 0 && lane < n) {
+        tokens[lane] = -1;
+        if (lps != nullptr) lps[lane] = 0.f;
+      }
+      if (lane == 0) s_draw.k = -1;
+      if (rank == 0 && lane == 0) {
+        set_status(a.status, kDevLenOob);
+        a.count[b] = 0;
+      }
+    } else {
+      const bool greedy = temp == 0.f, with_q = !greedy && draft != nullptr;
+      const float inv_t = greedy ? 1.f : 1.f / temp;
+      const bool in = lane >= nd || (id >= 0 && id < a.V);
+      const bool row_is_bad = lane <= nd && (ts.bad || (lane < nd && with_q && ds.bad));
+      float lp = 0.f;
+      bool ok = false;
+      if (lane < nd && in && !row_is_bad) {
+        const float y = (as_float(target[lane * a.target_row + id]) - ts.m) * inv_t;
+        const float qd = with_q ? expf((as_float(draft[lane * a.draft_row + id]) - ds.m) * inv_t) / ds.s : 1.f;
+        lp = y - logf(ts.s);
+        ok = greedy ? id == ts.best : u * qd < expf(y) / ts.s;
+      }
+      const unsigned stops = __ballot_sync(0xffffffffu, lane < nd && !ok);
+      const int k = stops != 0 ? __ffs(stops) - 1 : nd;
+      const bool bad = __shfl_sync(0xffffffffu, row_is_bad, k);
+      const bool draws = !bad && !greedy;
+      const float last_u = __shfl_sync(0xffffffffu, u, n - 1);
+      if (lane == k) {
+        const bool rejected = stops != 0;
+        s_draw = {draws ? k : -1, rejected ? id : -1, rejected && with_q, ts.m, ts.s, ds.m, ds.s, last_u};
+        if (rank == 0) {
+          a.count[b] = bad ? k : k + 1;
+          if (bad || !in) set_status(a.status, bad ? kDevLogits : kDevTokenOob);
+        }
+        if (greedy && !bad) {
+          id = ts.best;
+          lp = (as_float(target[k * a.target_row + id]) - ts.m) * inv_t - logf(ts.s);
+        }
+      }
+      if (rank == 0 && lane < n && (lane != k || !draws)) {  // a drawn token is written where it is found
+        const bool there = lane < k || (lane == k && !bad);
+        tokens[lane] = there ? id : -1;
+        if (lps != nullptr) lps[lane] = there ? lp : 0.f;
       }
     }
   }
-  const unsigned stops = __ballot_sync(0xffffffffu, lane < nd && !ok);
-  const int k = stops != 0 ? __ffs(stops) - 1 : nd;
-  const bool bad = __shfl_sync(0xffffffffu, row_is_bad, k);
-  const bool stray = __shfl_sync(0xffffffffu, !in, k);
-  if (writes) {
-    if (lane < n && (lane != k || bad)) {  // the token that follows is written where it is found
-      tokens[lane] = lane < k ? id : -1;
-      if (lps != nullptr) lps[lane] = lane < k ? lp : 0.f;
-    }
-    if (lane == 0) {
-      a.count[b] = bad ? k : k + 1;
-      if (bad || stray) set_status(a.status, bad ? kDevLogits : kDevTokenOob);
-    }
-  }
-  if (bad) return;
-  const RowStat pk = ts[k];
-  auto emit = [&](int pick) {
-    tokens[k] = pick;
-    if (lps != nullptr) lps[k] = (as_float(target[k * a.target_row + pick]) - pk.m) * inv_t - logf(pk.s);
-  };
-  if (greedy) {
-    if (writes && lane == 0) emit(pk.best);
-    return;
-  }
-  const bool rejected = stops != 0, minus = rejected && draft != nullptr;
-  FinalWeights<T> w = {target + k * a.target_row, minus ? draft + k * a.draft_row : nullptr, pk.m,
-                       minus ? ds[k].m : 0.0, 32.0 * 1.4426950408889634074 / static_cast<double>(temp), 1.0, 1.0,
-                       lane_factor(), rejected ? d[k] : -1, rejected};
+  asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA has started
+  __syncthreads();
+  const Draw d = s_draw;
+  if (d.k < 0) return;
+  const bool minus = d.minus != 0;
+  FinalWeights<T> w = {target + d.k * a.target_row, minus ? draft + d.k * a.draft_row : nullptr, d.pm, d.qm,
+                       32.0 * 1.4426950408889634074 / static_cast<double>(temp),
+                       minus ? static_cast<double>(d.ps) / d.qs : 0.0, factor, d.drafted};
   // warps take runs of columns, in order
-  const int runs = parts * kRowWarps, run = rank * kRowWarps + warp;
+  const int runs = parts * kFinalWarps, run = rank * kFinalWarps + warp;
   const int len = (a.V + 32 * runs - 1) / (32 * runs) * 32;
   const long long first = static_cast<long long>(run) * len;
   const int c0 = static_cast<int>(min(first, static_cast<long long>(a.V)));
   const int c1 = static_cast<int>(min(first + len, static_cast<long long>(a.V)));
-  auto share = [&](double* sums, double v) {  // to every CTA of the cluster
-    if (lane < parts) cluster.map_shared_rank(sums, lane)[run] = v;
-  };
-  double before = 0.0, total = 0.0;
-  cluster.sync();  // every CTA has started
+  double all_p = 0.0, all_q = 0.0, over_p = 0.0, over_q = 0.0;
   if (minus) {
-    double ps = 0.0, qs = 0.0;
-    warp_columns(w, true, c0, c1, [&](float xp, float xq, int) {
-      ps += w.pe(xp);
-      qs += w.qe(xq);
+    warp_columns(w.p, w.q, c0, c1, [&](float xp, float xq, int) {
+      const double e = w.pe(xp), f = w.qe(xq);
+      all_p += e;
+      all_q += f;
+      const bool over = e > w.r * f;
+      over_p += over ? e : 0.0;
+      over_q += over ? f : 0.0;
     });
-    share(s_p, warp_total(ps));
-    share(s_q, warp_total(qs));
-    cluster.sync();
-    warp_pick(s_p, runs, 0.0, &before, &total);
-    w.p_part = 1.0 / total;
-    warp_pick(s_q, runs, 0.0, &before, &total);
-    w.q_part = 1.0 / total;
+    all_q = warp_total(all_q), over_q = warp_total(over_q);
+  } else {
+    warp_columns(w.p, w.q, c0, c1, [&](float xp, float, int col) {
+      const double e = w.pe(xp);
+      all_p += e;
+      over_p += col == w.drafted ? 0.0 : e;
+    });
   }
-  const double u = a.uniforms[static_cast<size_t>(b) * n + n - 1];
-  const double* sums = s_w[0];
-  share(s_w[0], warp_weight(w, c0, c1));
+  all_p = warp_total(all_p), over_p = warp_total(over_p);
+  if (lane < parts) {  // to every CTA
+    double* to = cluster.map_shared_rank(&s_sum[0][0], lane) + run;
+    to[0] = all_p, to[kMost] = all_q, to[2 * kMost] = over_p, to[3 * kMost] = over_q;
+  }
   cluster.sync();
-  warp_pick(sums, runs, 0.0, &before, &total);
-  if (!(total > 0.0)) {  // q takes all of p away: draw from p
-    w.residual = false;
-    sums = s_w[1];
-    share(s_w[1], warp_weight(w, c0, c1));
-    cluster.sync();
-    warp_pick(sums, runs, 0.0, &before, &total);
+  // every warp picks the run; with r exact now
+  Running<kPer> sums;
+  auto entry = [&](int which, int i) { return i < runs ? s_sum[which][i] : 0.0; };
+  if (minus) {
+    double sp = 0.0, sq = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sp += entry(0, kPer * lane + i), sq += entry(1, kPer * lane + i);
+    w.r = warp_total(sp) / warp_total(sq);
   }
-  const double want = u * total;
-  const int mine = warp_pick(sums, runs, want, &before, &total);
-  if (mine / kRowWarps != rank) return;
-  // the run's CTA: a sixteenth of what is left to each warp, until two steps of 32 columns are left
-  long long lo = static_cast<long long>(mine) * len;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    sums.v[i] = fmax(entry(2, kPer * lane + i) - w.r * entry(3, kPer * lane + i), 0.0);
+  sums.scan();
+  if (!(sums.all > kNoWeight)) {  // q takes all of p away: draw from p
+    w.q = nullptr, w.drafted = -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sums.v[i] = entry(0, kPer * lane + i);
+    sums.scan();
+  }
+  const double want = static_cast<double>(d.u) * sums.all;
+  double before;
+  const int mine = sums.pick(want, &before);
+  if (mine / kFinalWarps != rank) return;
+  // the run's CTA: a sixteenth of what is left to each warp, until one step of 32 columns is left
+  const long long lo = static_cast<long long>(mine) * len;
   int hi = static_cast<int>(min(lo + len, static_cast<long long>(a.V))), from = static_cast<int>(lo);
-  while (hi - from > 64) {
-    const int sub = (hi - from + 32 * kRowWarps - 1) / (32 * kRowWarps) * 32;
+  while (hi - from > 32) {
+    const int sub = (hi - from + 32 * kFinalWarps - 1) / (32 * kFinalWarps) * 32;
     const int s0 = min(from + warp * sub, hi), s1 = min(s0 + sub, hi);
     const double v = warp_weight(w, s0, s1);
     if (lane == 0) s_sub[warp] = v;
     __syncthreads();
-    double skipped, all;
-    const int at = warp_pick(s_sub, kRowWarps, want - before, &skipped, &all);
+    Running<1> part;
+    part.v[0] = lane < kFinalWarps ? s_sub[lane] : 0.0;
     __syncthreads();
+    part.scan();
+    double skipped;
+    from += part.pick(want - before, &skipped) * sub;
     before += skipped;
-    from = from + max(at, 0) * sub;
     hi = min(from + sub, hi);
   }
   if (warp != 0) return;
-  int pick = -1, last = -1;
-  warp_columns(w, w.residual && w.q != nullptr, from, hi, [&](float xp, float xq, int col) {
-    const double v = w(xp, xq, col);
-    double scan = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += up;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && before + scan > want);
-    const unsigned any = __ballot_sync(0xffffffffu, v > 0.0);
-    if (pick < 0 && hit != 0) pick = col - lane + __ffs(hit) - 1;
-    if (any != 0) last = col - lane + 31 - __clz(any);
-    before += __shfl_sync(0xffffffffu, scan, 31);
-  });
-  if (lane == 0) emit(pick >= 0 ? pick : last);
+  const int c = from + lane;
+  Running<1> last;
+  last.v[0] = w(c < hi ? as_float(w.p[c]) : -INFINITY, c < hi && w.q != nullptr ? as_float(w.q[c]) : -INFINITY, c);
+  last.scan();
+  const int pick = min(from + last.pick(want - before, &before), a.V - 1);
+  if (lane == 0) {
+    const size_t o = static_cast<size_t>(b) * n + d.k;
+    a.tokens[o] = pick;
+    if (a.logprobs != nullptr) a.logprobs[o] = (as_float(w.p[pick]) - d.pm) / temp - logf(d.ps);
+  }
 }
 
 }  // namespace wmtp

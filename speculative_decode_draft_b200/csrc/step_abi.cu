@@ -39,13 +39,28 @@ bool heads_ok(const void* p, int64_t token_stride, int64_t head_stride, int byte
          head_stride * bytes % 16 == 0;
 }
 
-// CTAs that share each of `units` pieces of work on rows of `vocab` logits: more
-// while there are too few to fill the SMs and each still has two 16-byte
-// loads for every thread.
-int row_cluster(long long units, int vocab, int bytes, int sms) {
+template <typename F>
+F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
+  return dtype == WMTP_FP32 ? fp32 : dtype == WMTP_FP16 ? fp16 : bf16;
+}
+
+// CTAs that share each of `rows` rows: more while they are no more than five for
+// each SM (four are resident) and each keeps a whole batch.  Device time in us with
+// 1, 2, 4 CTAs a row of 131072 bf16, top 8: 4 rows 14.9, 12.1, 10.3; 300 rows 30.8,
+// 28.2, 35.3; 1024 rows 59.4, 73.6, 104.7.
+int row_cluster(long long rows, int vocab, int bytes, int sms) {
   int c = 1;
   const long long vecs = static_cast<long long>(vocab) * bytes / 16;
-  while (c < kMaxCluster && units * c < 2LL * sms && vecs / (2 * c) >= 2 * kRowThreads) c *= 2;
+  while (c < kRowCluster && rows * c * 2 <= 5LL * sms && vecs / (2 * c) >= kBatch) c *= 2;
+  return c;
+}
+
+// CTAs per sequence for the token that follows.  Device time in us of the whole call
+// with 2, 4, 8: 1 sequence of 3 drafts 24.8, 18.3, 14.9; 32 of 5 68.7, 61.9, 53.3;
+// 16 of 8 45.1, 34.7, 30.3.
+int final_cluster(long long batch, int vocab, int sms) {
+  int c = 1;
+  while (c < kFinalCluster && batch * c < 2LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;
   return c;
 }
 
@@ -179,14 +194,12 @@ wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, cons
   a.logprobs = logprobs_out, a.entropy = entropy_out, a.lse = lse_out, a.top_logprobs = top_logprobs_out;
   a.top_ids = top_ids_out, a.status = status_word;
   a.V = vocab, a.num_tokens = num_tokens, a.top_k = top_k;
-  auto kern = dtype == WMTP_FP32   ? logprob_kernel<float>
-              : dtype == WMTP_FP16 ? logprob_kernel<__half>
-                                   : logprob_kernel<__nv_bfloat16>;
   int dev = 0;
   DeviceInfo info;
   const wmtp_status s = current_device(&dev, &info);
   if (s != WMTP_OK) return s;
   const int c = row_cluster(rows, vocab, bytes, info.sms);
+  auto kern = by_dtype(dtype, logprob_kernel<float>, logprob_kernel<__half>, logprob_kernel<__nv_bfloat16>);
   return launch_clusters(true, kern, dim3(static_cast<unsigned>(rows) * c), dim3(kRowThreads), c,
                          static_cast<cudaStream_t>(stream), a);
 }
@@ -225,20 +238,18 @@ wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32
   a.B = batch, a.num_q = num_q, a.V = vocab;
   const unsigned rows = static_cast<unsigned>(batch) * (num_q + (a.draft != nullptr ? num_q - 1 : 0));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto rows_kern = dtype == WMTP_FP32   ? accept_rows_kernel<float>
-                   : dtype == WMTP_FP16 ? accept_rows_kernel<__half>
-                                        : accept_rows_kernel<__nv_bfloat16>;
-  auto kern = dtype == WMTP_FP32 ? accept_kernel<float> : dtype == WMTP_FP16 ? accept_kernel<__half>
-                                                                             : accept_kernel<__nv_bfloat16>;
   int dev = 0;
   DeviceInfo info;
   wmtp_status s = current_device(&dev, &info);
   if (s != WMTP_OK) return s;
   int c = row_cluster(rows, vocab, bytes, info.sms);
+  auto rows_kern =
+      by_dtype(dtype, accept_rows_kernel<float>, accept_rows_kernel<__half>, accept_rows_kernel<__nv_bfloat16>);
   s = launch_clusters(true, rows_kern, dim3(rows * c), dim3(kRowThreads), c, st, a);
   if (s != WMTP_OK) return s;
-  c = row_cluster(batch, vocab, bytes, info.sms);
-  return launch_clusters(true, kern, dim3(static_cast<unsigned>(batch) * c), dim3(kRowThreads), c, st, a);
+  c = final_cluster(batch, vocab, info.sms);
+  auto kern = by_dtype(dtype, accept_kernel<float>, accept_kernel<__half>, accept_kernel<__nv_bfloat16>);
+  return launch_clusters(true, kern, dim3(static_cast<unsigned>(batch) * c), dim3(kFinalThreads), c, st, a);
 }
 
 }  // extern "C"
