@@ -75,8 +75,8 @@ typedef struct {
  *                cache stay as they were
  *   slots      : [tokens] int64 cache slots, page * page_size + row, or NULL to
  *                write no cache; -1 writes nothing for that token, any other
- *                slot outside the pool too, and sets WMTP_DEV_PAGE_OOB.  Two
- *                tokens with one slot: one of them is stored.
+ *                slot outside the pool too, and sets WMTP_DEV_PAGE_OOB.  No
+ *                two tokens have one slot (what it holds would be any mixture).
  *   kv         : with slots: k_pool, v_pool and num_pages are used
  *   v          : with slots, else NULL
  *   q_weight, k_weight : [head_dim] of weight_dtype (WMTP_BF16 or WMTP_FP32), or NULL

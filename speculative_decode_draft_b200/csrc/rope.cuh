@@ -12,7 +12,9 @@
 
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <string.h>
 
+#include "f32x2.cuh"
 #include "status.cuh"
 
 namespace wmtp {
@@ -20,6 +22,7 @@ namespace wmtp {
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = 32 * kRopeWarps;
 constexpr int kRopeMaxDim = 256;
+constexpr int kRopeRows = 2;  // loaded before the first is used
 
 struct RopeArgs {
   const void *q, *k, *v;  // NULL: absent
@@ -37,32 +40,50 @@ struct RopeArgs {
   float factor;
   __nv_bfloat16 *q_out, *k_out;
   int tokens, Hq, Hkv, D;
+  int lanes, slices, per_slice;
+  float inv_dim;
   int32_t* status;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// P elements, read and written at once.
+template <int Bytes>
+struct Raw;
+template <>
+struct Raw<2> {
+  using Type = uint16_t;
+};
+template <>
+struct Raw<4> {
+  using Type = uint32_t;
+};
+template <>
+struct Raw<8> {
+  using Type = uint2;
+};
+template <>
+struct Raw<16> {
+  using Type = uint4;
+};
+
+template <typename In, int P>
+struct Chunk {
+  using Type = typename Raw<P * sizeof(In)>::Type;
+  static __device__ __forceinline__ Type load(const In* p) { return *reinterpret_cast<const Type*>(p); }
+  static __device__ __forceinline__ void widen(Type raw, float (&x)[P]) {
+    In h[P];
+    memcpy(h, &raw, sizeof(raw));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < P; ++i) x[i] = static_cast<float>(h[i]);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
+  static __device__ __forceinline__ void store(In* p, const float (&x)[P]) {  // In is bf16
+    In h[P];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < P; ++i) h[i] = __float2bfloat16_rn(x[i]);
+    Type raw;
+    memcpy(&raw, h, sizeof(raw));
+    *reinterpret_cast<Type*>(p) = raw;
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+};
 
 // cos and sin of pair i at position t.
 __device__ __forceinline__ float2 rope_turn(const RopeArgs& a, int t, int i) {
@@ -73,80 +94,213 @@ __device__ __forceinline__ float2 rope_turn(const RopeArgs& a, int t, int i) {
   return make_float2(c * a.factor, s * a.factor);
 }
 
-// One warp per head row (of q, k or v) of a token; a lane holds 8 elements.
-template <typename In>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
-  __shared__ float s_row[kRopeWarps][kRopeMaxDim];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nq = a.q != nullptr ? a.Hq : 0, nk = a.k != nullptr ? a.Hkv : 0, nv = a.v != nullptr ? a.Hkv : 0;
-  const long long row = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
-  const int per = nq + nk + nv;
-  if (row >= static_cast<long long>(a.tokens) * per) return;
-  const int t = static_cast<int>(row / per);
-  int h = static_cast<int>(row % per);
-  const int pos = a.positions[t];
-  if (pos < 0) return;
-  const int e = lane * 8;
-  const bool live = e < a.D;
-  const int kind = h < nq ? 0 : h < nq + nk ? 1 : 2;
-  h -= kind == 0 ? 0 : kind == 1 ? nq : nq + nk;
-  const In* src = static_cast<const In*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                  t * (kind == 0 ? a.q_token : kind == 1 ? a.k_token : a.v_token) +
-                  h * (kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head);
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) load8(src + e, x);
-  const void* w = kind == 0 ? a.qw : kind == 1 ? a.kw : nullptr;
-  if (w != nullptr) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss / a.D + a.eps);
-    if (live) {
-      float g[8];
-      if (a.weight_f32)
-        load8(static_cast<const float*>(w) + e, g);
-      else
-        load8(static_cast<const __nv_bfloat16*>(w) + e, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (g[i] + a.offset);
-    }
+// A group of `lanes` (D / 8, rounded up to a power of two) takes a slice of a
+// token's head rows.  A lane holds four pairs of a row, a[i] and b[i], so that
+// the pairs' cosines serve all its rows.  They are read and written as chunks
+// of P elements: for the half layout the a's at c and the b's at
+// c + rotary_dim / 2 (P = 4 where that is a multiple of 4, else 2 or 1), for
+// the interleaved layout as they stand.  Elements behind rotary_dim go as pairs
+// that are not turned.
+template <typename In, int P, bool kInterleaved>
+struct RopeLane {
+  static constexpr int kChunks = 8 / P;
+  int at[kChunks];     // element of each chunk
+  bool live[kChunks];  // inside the head
+  bool turned[4];
+  uint64_t cos2[2], sin2[2], minus_sin2[2];
+
+  // Which of the lane's eight values chunk c holds at i: a[j] or b[j].
+  static __device__ __forceinline__ constexpr int pair(int c, int i) {
+    return kInterleaved ? (c * P + i) / 2 : c / 2 * P + i;
   }
-  if (kind != 2 && a.rotary_dim > 0) {
-    if (live)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_row[warp][e + i] = x[i];
-    __syncwarp();
+  static __device__ __forceinline__ constexpr bool is_b(int c, int i) { return kInterleaved ? i % 2 : c % 2; }
+
+  __device__ __forceinline__ void place(const RopeArgs& a, int lane) {
     const int half = a.rotary_dim / 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = e + i;
-      if (c >= a.rotary_dim) continue;
-      const bool second = a.interleaved ? (c & 1) != 0 : c >= half;
-      const int pair = a.interleaved ? c >> 1 : second ? c - half : c;
-      const int other = a.interleaved ? c ^ 1 : second ? c - half : c + half;
-      const float2 cs = rope_turn(a, pos, pair);
-      const float o = s_row[warp][other];
-      x[i] = second ? x[i] * cs.x + o * cs.y : x[i] * cs.x - o * cs.y;
+    for (int c = 0; c < kChunks; ++c) {
+      if (kInterleaved) {
+        at[c] = lane * 8 + c * P;
+        live[c] = at[c] < a.D;
+      } else {
+        const int first = (lane + c / 2 * a.lanes) * P;  // of the pair of chunks
+        live[c] = 2 * first < a.D;
+        at[c] = first >= half ? 2 * first + c % 2 * P : first + c % 2 * half;
+      }
     }
   }
-  if (!live) return;
-  if (kind == 0) {
-    store8(a.q_out + (static_cast<long long>(t) * a.Hq + h) * a.D + e, x);
-    return;
-  }
-  if (kind == 1 && a.k_out != nullptr) store8(a.k_out + (static_cast<long long>(t) * a.Hkv + h) * a.D + e, x);
-  if (a.slots != nullptr) {
-    const long long slot = a.slots[t];
-    if (slot >= 0 && slot < a.num_slots) {
-      const long long page = slot / a.page_size, r = slot % a.page_size;
-      store8((kind == 1 ? a.k_pool : a.v_pool) + ((page * a.Hkv + h) * a.page_size + r) * a.D + e, x);
-    } else if (slot != -1) {
-      set_status(a.status, kDevPageOob);
+  __device__ __forceinline__ void turn(const RopeArgs& a, int lane, int pos) {
+    const int half = a.rotary_dim / 2;
+    float2 cs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = kInterleaved ? lane * 4 + i : (lane + i / P * a.lanes) * P + i % P;
+      turned[i] = j < half;
+      cs[i] = turned[i] ? rope_turn(a, pos, j) : make_float2(1.f, 0.f);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      cos2[i] = pack2(cs[2 * i].x, cs[2 * i + 1].x);
+      sin2[i] = pack2(cs[2 * i].y, cs[2 * i + 1].y);
+      minus_sin2[i] = pack2(-cs[2 * i].y, -cs[2 * i + 1].y);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, typename Chunk<T, P>::Type (&raw)[kChunks]) const {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      if (live[c]) raw[c] = Chunk<T, P>::load(row + at[c]);
+  }
+  template <typename T>
+  __device__ __forceinline__ void widen(const typename Chunk<T, P>::Type (&raw)[kChunks], float (&a)[4], float (&b)[4]) const {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float x[P];
+      Chunk<T, P>::widen(raw[c], x);
+#pragma unroll
+      for (int i = 0; i < P; ++i) (is_b(c, i) ? b : a)[pair(c, i)] = live[c] ? x[i] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* row, const float (&a)[4], const float (&b)[4]) const {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float x[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[i] = (is_b(c, i) ? b : a)[pair(c, i)];
+      if (live[c]) Chunk<__nv_bfloat16, P>::store(row + at[c], x);
+    }
+  }
+};
+
+__device__ __forceinline__ void pack4(const float (&x)[4], uint64_t (&p)[2]) {
+  p[0] = pack2(x[0], x[1]), p[1] = pack2(x[2], x[3]);
+}
+__device__ __forceinline__ void unpack4(const uint64_t (&p)[2], float (&x)[4]) {
+  unpack2(p[0], x[0], x[1]), unpack2(p[1], x[2], x[3]);
+}
+
+// Rows [r0, r1) of queries or of keys: norm, turn, store.  `src`, `out`,
+// `cache`: of row 0 (out, cache may be NULL).
+template <typename In, int P, bool kInterleaved>
+__device__ __forceinline__ void rope_rows(const RopeArgs& args, const RopeLane<In, P, kInterleaved>& l, unsigned mask, int r0,
+                                          int r1, const In* src, long long src_step, const void* weight, __nv_bfloat16* out,
+                                          __nv_bfloat16* cache, long long cache_step) {
+  using L = RopeLane<In, P, kInterleaved>;
+  float a[4], b[4];
+  uint64_t ga[2], gb[2];
+  if (weight != nullptr) {
+    const uint64_t offset = pack2(args.offset, args.offset);
+    if (args.weight_f32) {
+      if constexpr (P * sizeof(float) <= 16) {
+        typename Chunk<float, P>::Type raw[L::kChunks];
+        l.load(static_cast<const float*>(weight), raw);
+        l.template widen<float>(raw, a, b);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 w = l.live[0] ? reinterpret_cast<const float2*>(static_cast<const float*>(weight) + l.at[0])[i]
+                                     : make_float2(0.f, 0.f);
+          a[i] = w.x, b[i] = w.y;
+        }
+      }
+    } else {
+      typename Chunk<__nv_bfloat16, P>::Type raw[L::kChunks];
+      l.load(static_cast<const __nv_bfloat16*>(weight), raw);
+      l.template widen<__nv_bfloat16>(raw, a, b);
+    }
+    pack4(a, ga), pack4(b, gb);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ga[i] = add2(ga[i], offset), gb[i] = add2(gb[i], offset);
+  }
+  const bool partly = args.rotary_dim < args.D;
+  src += r0 * src_step;
+  for (int r = r0; r < r1; r += kRopeRows) {
+    typename Chunk<In, P>::Type raw[kRopeRows][L::kChunks];
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      if (r + u < r1) l.load(src, raw[u]);
+      src += src_step;
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      if (r + u >= r1) break;
+      uint64_t a2[2], b2[2];
+      l.template widen<In>(raw[u], a, b);
+      pack4(a, a2), pack4(b, b2);
+      if (weight != nullptr) {
+        uint64_t s2 = mul2(a2[0], a2[0]);
+        s2 = fma2(a2[1], a2[1], s2);
+        s2 = fma2(b2[0], b2[0], s2);
+        s2 = fma2(b2[1], b2[1], s2);
+        float s, t;
+        unpack2(s2, s, t);
+        s += t;
+        for (int o = args.lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+        const float scale = rsqrtf(fmaf(s, args.inv_dim, args.eps));
+        const uint64_t scale2 = pack2(scale, scale);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a2[i] = mul2(mul2(a2[i], scale2), ga[i]);
+          b2[i] = mul2(mul2(b2[i], scale2), gb[i]);
+        }
+      }
+      uint64_t c2[2], d2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        c2[i] = fma2(a2[i], l.cos2[i], mul2(b2[i], l.minus_sin2[i]));
+        d2[i] = fma2(b2[i], l.cos2[i], mul2(a2[i], l.sin2[i]));
+      }
+      float c[4], d[4];
+      unpack4(c2, c), unpack4(d2, d);
+      if (partly) {  // not by cos 1 and sin 0: an infinity beside would leave NaN
+        unpack4(a2, a), unpack4(b2, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!l.turned[i]) c[i] = a[i], d[i] = b[i];
+      }
+      if (out != nullptr) l.store(out + static_cast<long long>(r + u) * args.D, c, d);
+      if (cache != nullptr) l.store(cache + (r + u) * cache_step, c, d);
+    }
+  }
+}
+
+template <typename In, int P, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lanes = a.lanes, lane = threadIdx.x & (lanes - 1), sub = (threadIdx.x & 31) & ~(lanes - 1);
+  const unsigned mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << sub;
+  const long long group = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) / lanes;
+  const int t = static_cast<int>(group / a.slices), slice = static_cast<int>(group - static_cast<long long>(t) * a.slices);
+  if (t >= a.tokens) return;
+  const int pos = a.positions[t];
+  if (pos < 0) return;
+  const int nq = a.q != nullptr ? a.Hq : 0, nk = a.k != nullptr ? a.Hkv : 0, nv = a.v != nullptr ? a.Hkv : 0;
+  const int rows = nq + nk + nv, r0 = slice * a.per_slice, r1 = min(r0 + a.per_slice, rows);
+  RopeLane<In, P, kInterleaved> l;
+  l.place(a, lane);
+  if (r0 < nq + nk) l.turn(a, lane, pos);
+  if (r0 < nq)
+    rope_rows(a, l, mask, r0, min(r1, nq), static_cast<const In*>(a.q) + t * a.q_token, a.q_head, a.qw,
+              a.q_out + static_cast<long long>(t) * a.Hq * a.D, nullptr, 0);
+  if (r1 <= nq) return;
+  const long long slot = a.slots != nullptr ? a.slots[t] : -1;
+  const bool cached = slot >= 0 && slot < a.num_slots;
+  if (!cached && slot != -1 && lane == 0) set_status(a.status, kDevPageOob);
+  const long long page = cached ? slot / a.page_size : 0, in_page = cached ? slot - page * a.page_size : 0;
+  const long long cell = (page * a.Hkv * a.page_size + in_page) * a.D, step = static_cast<long long>(a.page_size) * a.D;
+  const int k0 = max(r0 - nq, 0), k1 = min(r1 - nq, nk);
+  if (k0 < k1)
+    rope_rows(a, l, mask, k0, k1, static_cast<const In*>(a.k) + t * a.k_token, a.k_head, a.kw,
+              a.k_out != nullptr ? a.k_out + static_cast<long long>(t) * a.Hkv * a.D : nullptr,
+              cached ? a.k_pool + cell : nullptr, step);
+  if (!cached) return;
+  for (int h = max(r0 - nq - nk, 0); h < r1 - nq - nk; ++h) {
+    typename Chunk<In, P>::Type raw[8 / P];
+    float x[4], y[4];
+    l.load(static_cast<const In*>(a.v) + t * a.v_token + h * a.v_head, raw);
+    l.template widen<In>(raw, x, y);
+    l.store(a.v_pool + cell + h * step, x, y);
   }
 }
 

@@ -44,6 +44,16 @@ F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
   return dtype == WMTP_FP32 ? fp32 : dtype == WMTP_FP16 ? fp16 : bf16;
 }
 
+// Slices of a token's head rows, one for each group of lanes: as few as leave 64
+// warps for each SM.
+int rope_slices(long long tokens, int rows, int lanes) {
+#ifdef FORCE_S
+  return FORCE_S < rows ? FORCE_S : rows;
+#endif
+  const long long want = 148LL * 64 * 32 / lanes, n = (want + tokens - 1) / tokens;
+  return n < rows ? static_cast<int>(n) : rows;
+}
+
 // CTAs that share each of `rows` rows: more while they are no more than five for
 // each SM (four are resident) and each keeps a whole batch.  Device time in us with
 // 1, 2, 4 CTAs a row of 131072 bf16, top 8: 4 rows 14.9, 12.1, 10.3; 300 rows 30.8,
@@ -138,9 +148,25 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
   a.tokens = tokens, a.Hq = params->num_heads_q, a.Hkv = params->num_heads_kv, a.D = D;
   a.status = status_word;
   const int rows = (q != nullptr ? a.Hq : 0) + (k != nullptr ? a.Hkv : 0) + (v != nullptr ? a.Hkv : 0);
-  const long long grid = (static_cast<long long>(tokens) * rows + kRopeWarps - 1) / kRopeWarps;
+  a.inv_dim = 1.f / D;
+  a.lanes = 1;
+  while (a.lanes * 8 < D) a.lanes *= 2;
+  a.slices = rope_slices(tokens, rows, a.lanes);
+  a.per_slice = (rows + a.slices - 1) / a.slices;
+  a.slices = (rows + a.per_slice - 1) / a.per_slice;
+  const int groups = kRopeThreads / a.lanes;
+  const long long grid = (static_cast<long long>(tokens) * a.slices + groups - 1) / groups;
   if (grid > kMaxGridX) return WMTP_ERR_UNSUPPORTED;
-  auto kern = in_dtype == WMTP_FP32 ? rope_kernel<float> : rope_kernel<__nv_bfloat16>;
+  const int half = a.rotary_dim / 2;
+  const int chunk = half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+  auto pick = [&](auto in) {
+    using In = decltype(in);
+    return a.interleaved ? rope_kernel<In, 16 / sizeof(In), true>
+           : chunk == 4  ? rope_kernel<In, 4, false>
+           : chunk == 2  ? rope_kernel<In, 2, false>
+                         : rope_kernel<In, 1, false>;
+  };
+  auto kern = in_dtype == WMTP_FP32 ? pick(float()) : pick(__nv_bfloat16());
   return launch_plain(true, kern, dim3(static_cast<unsigned>(grid)), dim3(kRopeThreads),
                       static_cast<cudaStream_t>(stream), a);
 }

@@ -79,8 +79,6 @@ NONE = (None, 0, 0)
     (dict(qw=A + 8), INVALID),
     (dict(q_out=A + 8), INVALID),
     (dict(k_out=A + 8), INVALID),
-    (dict(heads=(65535, 65535), tokens=2000000, k=(A, 16776960, 256), q=(A, 16776960, 256), v=(A, 16776960, 256)),
-     UNSUPPORTED),
 ])
 def test_qk_norm_rope_refuses(lib, kw, code):
     assert _rope(lib, **kw) == code
