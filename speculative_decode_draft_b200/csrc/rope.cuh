@@ -70,18 +70,34 @@ struct Chunk {
   using Type = typename Raw<P * sizeof(In)>::Type;
   static __device__ __forceinline__ Type load(const In* p) { return *reinterpret_cast<const Type*>(p); }
   static __device__ __forceinline__ void widen(Type raw, float (&x)[P]) {
-    In h[P];
-    memcpy(h, &raw, sizeof(raw));
+    if constexpr (sizeof(In) == 4) {
+      memcpy(x, &raw, sizeof(raw));
+    } else if constexpr (P == 1) {
+      x[0] = __uint_as_float(static_cast<uint32_t>(raw) << 16);
+    } else {
+      uint32_t w[P / 2];
+      memcpy(w, &raw, sizeof(raw));
 #pragma unroll
-    for (int i = 0; i < P; ++i) x[i] = static_cast<float>(h[i]);
+      for (int i = 0; i < P / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
   }
   static __device__ __forceinline__ void store(In* p, const float (&x)[P]) {  // In is bf16
-    In h[P];
+    if constexpr (P == 1) {
+      *p = __float2bfloat16_rn(x[0]);
+    } else {
+      uint32_t w[P / 2];
 #pragma unroll
-    for (int i = 0; i < P; ++i) h[i] = __float2bfloat16_rn(x[i]);
-    Type raw;
-    memcpy(&raw, h, sizeof(raw));
-    *reinterpret_cast<Type*>(p) = raw;
+      for (int i = 0; i < P / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        memcpy(&w[i], &h, 4);
+      }
+      Type raw;
+      memcpy(&raw, w, sizeof(raw));
+      *reinterpret_cast<Type*>(p) = raw;
+    }
   }
 };
 
@@ -100,8 +116,9 @@ __device__ __forceinline__ float2 rope_turn(const RopeArgs& a, int t, int i) {
 // of P elements: for the half layout the a's at c and the b's at
 // c + rotary_dim / 2 (P = 4 where that is a multiple of 4, else 2 or 1), for
 // the interleaved layout as they stand.  Elements behind rotary_dim go as pairs
-// that are not turned.
-template <typename In, int P, bool kInterleaved>
+// that are not turned.  kLanes: the group's lanes where they hold exactly a
+// head (D = 8, 16, 32 lanes' 8), else 0.
+template <typename In, int P, bool kInterleaved, int kLanes>
 struct RopeLane {
   static constexpr int kChunks = 8 / P;
   int at[kChunks];     // element of each chunk
@@ -121,10 +138,10 @@ struct RopeLane {
     for (int c = 0; c < kChunks; ++c) {
       if (kInterleaved) {
         at[c] = lane * 8 + c * P;
-        live[c] = at[c] < a.D;
+        live[c] = kLanes != 0 || at[c] < a.D;
       } else {
         const int first = (lane + c / 2 * a.lanes) * P;  // of the pair of chunks
-        live[c] = 2 * first < a.D;
+        live[c] = kLanes != 0 || 2 * first < a.D;
         at[c] = first >= half ? 2 * first + c % 2 * P : first + c % 2 * half;
       }
     }
@@ -149,7 +166,7 @@ struct RopeLane {
   __device__ __forceinline__ void load(const T* row, typename Chunk<T, P>::Type (&raw)[kChunks]) const {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
-      if (live[c]) raw[c] = Chunk<T, P>::load(row + at[c]);
+      if (kLanes != 0 || live[c]) raw[c] = Chunk<T, P>::load(row + at[c]);
   }
   template <typename T>
   __device__ __forceinline__ void widen(const typename Chunk<T, P>::Type (&raw)[kChunks], float (&a)[4], float (&b)[4]) const {
@@ -158,7 +175,7 @@ struct RopeLane {
       float x[P];
       Chunk<T, P>::widen(raw[c], x);
 #pragma unroll
-      for (int i = 0; i < P; ++i) (is_b(c, i) ? b : a)[pair(c, i)] = live[c] ? x[i] : 0.f;
+      for (int i = 0; i < P; ++i) (is_b(c, i) ? b : a)[pair(c, i)] = kLanes != 0 || live[c] ? x[i] : 0.f;
     }
   }
   __device__ __forceinline__ void store(__nv_bfloat16* row, const float (&a)[4], const float (&b)[4]) const {
@@ -167,7 +184,7 @@ struct RopeLane {
       float x[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) x[i] = (is_b(c, i) ? b : a)[pair(c, i)];
-      if (live[c]) Chunk<__nv_bfloat16, P>::store(row + at[c], x);
+      if (kLanes != 0 || live[c]) Chunk<__nv_bfloat16, P>::store(row + at[c], x);
     }
   }
 };
@@ -181,11 +198,11 @@ __device__ __forceinline__ void unpack4(const uint64_t (&p)[2], float (&x)[4]) {
 
 // Rows [r0, r1) of queries or of keys: norm, turn, store.  `src`, `out`,
 // `cache`: of row 0 (out, cache may be NULL).
-template <typename In, int P, bool kInterleaved>
-__device__ __forceinline__ void rope_rows(const RopeArgs& args, const RopeLane<In, P, kInterleaved>& l, unsigned mask, int r0,
+template <typename In, int P, bool kInterleaved, int kLanes>
+__device__ __forceinline__ void rope_rows(const RopeArgs& args, const RopeLane<In, P, kInterleaved, kLanes>& l, unsigned mask, int r0,
                                           int r1, const In* src, long long src_step, const void* weight, __nv_bfloat16* out,
                                           __nv_bfloat16* cache, long long cache_step) {
-  using L = RopeLane<In, P, kInterleaved>;
+  using L = RopeLane<In, P, kInterleaved, kLanes>;
   float a[4], b[4];
   uint64_t ga[2], gb[2];
   if (weight != nullptr) {
@@ -214,61 +231,77 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& args, const RopeLane<I
   }
   const bool partly = args.rotary_dim < args.D;
   src += r0 * src_step;
-  for (int r = r0; r < r1; r += kRopeRows) {
-    typename Chunk<In, P>::Type raw[kRopeRows][L::kChunks];
+  if (out != nullptr) out += static_cast<long long>(r0) * args.D;
+  if (cache != nullptr) cache += r0 * cache_step;
+  auto row = [&](const typename Chunk<In, P>::Type (&raw)[L::kChunks]) {
+    uint64_t a2[2], b2[2];
+    l.template widen<In>(raw, a, b);
+    pack4(a, a2), pack4(b, b2);
+    if (weight != nullptr) {
+      uint64_t s2 = mul2(a2[0], a2[0]);
+      s2 = fma2(a2[1], a2[1], s2);
+      s2 = fma2(b2[0], b2[0], s2);
+      s2 = fma2(b2[1], b2[1], s2);
+      float s, t;
+      unpack2(s2, s, t);
+      s += t;
+      if constexpr (kLanes != 0) {
 #pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      if (r + u < r1) l.load(src, raw[u]);
-      src += src_step;
-    }
-#pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      if (r + u >= r1) break;
-      uint64_t a2[2], b2[2];
-      l.template widen<In>(raw[u], a, b);
-      pack4(a, a2), pack4(b, b2);
-      if (weight != nullptr) {
-        uint64_t s2 = mul2(a2[0], a2[0]);
-        s2 = fma2(a2[1], a2[1], s2);
-        s2 = fma2(b2[0], b2[0], s2);
-        s2 = fma2(b2[1], b2[1], s2);
-        float s, t;
-        unpack2(s2, s, t);
-        s += t;
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+      } else {
         for (int o = args.lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
-        const float scale = rsqrtf(fmaf(s, args.inv_dim, args.eps));
-        const uint64_t scale2 = pack2(scale, scale);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a2[i] = mul2(mul2(a2[i], scale2), ga[i]);
-          b2[i] = mul2(mul2(b2[i], scale2), gb[i]);
-        }
       }
-      uint64_t c2[2], d2[2];
+      const float scale = rsqrtf(fmaf(s, args.inv_dim, args.eps));
+      const uint64_t scale2 = pack2(scale, scale);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        c2[i] = fma2(a2[i], l.cos2[i], mul2(b2[i], l.minus_sin2[i]));
-        d2[i] = fma2(b2[i], l.cos2[i], mul2(a2[i], l.sin2[i]));
+        a2[i] = mul2(mul2(a2[i], scale2), ga[i]);
+        b2[i] = mul2(mul2(b2[i], scale2), gb[i]);
       }
-      float c[4], d[4];
-      unpack4(c2, c), unpack4(d2, d);
-      if (partly) {  // not by cos 1 and sin 0: an infinity beside would leave NaN
-        unpack4(a2, a), unpack4(b2, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!l.turned[i]) c[i] = a[i], d[i] = b[i];
-      }
-      if (out != nullptr) l.store(out + static_cast<long long>(r + u) * args.D, c, d);
-      if (cache != nullptr) l.store(cache + (r + u) * cache_step, c, d);
     }
+    uint64_t c2[2], d2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c2[i] = fma2(a2[i], l.cos2[i], mul2(b2[i], l.minus_sin2[i]));
+      d2[i] = fma2(b2[i], l.cos2[i], mul2(a2[i], l.sin2[i]));
+    }
+    float c[4], d[4];
+    unpack4(c2, c), unpack4(d2, d);
+    if (partly) {  // not by cos 1 and sin 0: an infinity beside would leave NaN
+      unpack4(a2, a), unpack4(b2, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!l.turned[i]) c[i] = a[i], d[i] = b[i];
+    }
+    if (out != nullptr) {
+      l.store(out, c, d);
+      out += args.D;
+    }
+    if (cache != nullptr) {
+      l.store(cache, c, d);
+      cache += cache_step;
+    }
+  };
+  int r = r0;
+  for (; r + kRopeRows <= r1; r += kRopeRows) {
+    typename Chunk<In, P>::Type raw[kRopeRows][L::kChunks];
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u, src += src_step) l.load(src, raw[u]);
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) row(raw[u]);
+  }
+  for (; r < r1; ++r, src += src_step) {
+    typename Chunk<In, P>::Type raw[L::kChunks];
+    l.load(src, raw);
+    row(raw);
   }
 }
 
-template <typename In, int P, bool kInterleaved>
+template <typename In, int P, bool kInterleaved, int kLanes>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lanes = a.lanes, lane = threadIdx.x & (lanes - 1), sub = (threadIdx.x & 31) & ~(lanes - 1);
+  const int lanes = kLanes != 0 ? kLanes : a.lanes, lane = threadIdx.x & (lanes - 1), sub = (threadIdx.x & 31) & ~(lanes - 1);
   const unsigned mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << sub;
   const long long group = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) / lanes;
   const int t = static_cast<int>(group / a.slices), slice = static_cast<int>(group - static_cast<long long>(t) * a.slices);
@@ -277,7 +310,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(RopeArgs a) {
   if (pos < 0) return;
   const int nq = a.q != nullptr ? a.Hq : 0, nk = a.k != nullptr ? a.Hkv : 0, nv = a.v != nullptr ? a.Hkv : 0;
   const int rows = nq + nk + nv, r0 = slice * a.per_slice, r1 = min(r0 + a.per_slice, rows);
-  RopeLane<In, P, kInterleaved> l;
+  RopeLane<In, P, kInterleaved, kLanes> l;
   l.place(a, lane);
   if (r0 < nq + nk) l.turn(a, lane, pos);
   if (r0 < nq)

@@ -44,14 +44,13 @@ F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
   return dtype == WMTP_FP32 ? fp32 : dtype == WMTP_FP16 ? fp16 : bf16;
 }
 
-// Slices of a token's head rows, one for each group of lanes: as few as leave 64
-// warps for each SM.
+// Slices of a token's head rows, one for each group of lanes: as many as fit the
+// 32 warps that each SM holds at once; one where the tokens alone fill them, since each
+// slice works its angles out again.  Device time in us of 20 rows of 256 with 1, 3, 10
+// slices: 16 tokens 8.6, 4.6, 3.2; 1537 15.2, 9.6, 13.6; 4096 21.0, 24.1, 32.4.
 int rope_slices(long long tokens, int rows, int lanes) {
-#ifdef FORCE_S
-  return FORCE_S < rows ? FORCE_S : rows;
-#endif
-  const long long want = 148LL * 64 * 32 / lanes, n = (want + tokens - 1) / tokens;
-  return n < rows ? static_cast<int>(n) : rows;
+  const long long n = 148LL * 32 * 32 / lanes / tokens;
+  return n < 1 ? 1 : n < rows ? static_cast<int>(n) : rows;
 }
 
 // CTAs that share each of `rows` rows: more while they are no more than five for
@@ -159,12 +158,21 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
   if (grid > kMaxGridX) return WMTP_ERR_UNSUPPORTED;
   const int half = a.rotary_dim / 2;
   const int chunk = half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+  const int full = a.lanes * 8 == D ? a.lanes : 0;
   auto pick = [&](auto in) {
     using In = decltype(in);
-    return a.interleaved ? rope_kernel<In, 16 / sizeof(In), true>
-           : chunk == 4  ? rope_kernel<In, 4, false>
-           : chunk == 2  ? rope_kernel<In, 2, false>
-                         : rope_kernel<In, 1, false>;
+    constexpr int kRun = 16 / sizeof(In);
+    if (a.interleaved)
+      return full == 32   ? rope_kernel<In, kRun, true, 32>
+             : full == 16 ? rope_kernel<In, kRun, true, 16>
+             : full == 8  ? rope_kernel<In, kRun, true, 8>
+                          : rope_kernel<In, kRun, true, 0>;
+    if (chunk == 4)
+      return full == 32   ? rope_kernel<In, 4, false, 32>
+             : full == 16 ? rope_kernel<In, 4, false, 16>
+             : full == 8  ? rope_kernel<In, 4, false, 8>
+                          : rope_kernel<In, 4, false, 0>;
+    return chunk == 2 ? rope_kernel<In, 2, false, 0> : rope_kernel<In, 1, false, 0>;
   };
   auto kern = in_dtype == WMTP_FP32 ? pick(float()) : pick(__nv_bfloat16());
   return launch_plain(true, kern, dim3(static_cast<unsigned>(grid)), dim3(kRopeThreads),
