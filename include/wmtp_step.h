@@ -128,6 +128,9 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
  *                page * page_size + row; rows behind the last token are -1.
  *                Both are what wmtp_qk_norm_rope takes.  A token on a page
  *                outside [0, num_pages) has slot -1, WMTP_DEV_PAGE_OOB.
+ *   workspace  : 256-byte aligned device scratch.  Call with workspace and
+ *                free_pages NULL to get the size in *workspace_bytes; where it
+ *                is 0 workspace may be NULL.
  * A page belongs to one sequence: a page that two rows of the table share would
  * be returned by each.  The buffers do not overlap.
  * page_size as wmtp.h; max_pages * page_size <= 2^30.
@@ -135,7 +138,8 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
 wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t* page_table, int32_t max_pages,
                               int32_t* kv_len, const int32_t* new_len, int32_t* free_pages, int32_t* free_count,
                               int32_t num_pages, int32_t* cu_tokens, int32_t* positions, int64_t* slots,
-                              int32_t max_tokens, int32_t* status_word, void* stream);
+                              int32_t max_tokens, void* workspace, size_t* workspace_bytes, int32_t* status_word,
+                              void* stream);
 
 /*
  * wmtp_token_logprobs -- log probabilities of given tokens, with the entropy

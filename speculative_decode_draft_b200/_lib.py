@@ -207,7 +207,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                       c_float, c_float, c_void_p, c_void_p, i32p, c_void_p]
     lib.wmtp_pages_resize.restype = c_int32
     lib.wmtp_pages_resize.argtypes = [PP, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
-                                      c_int32, c_void_p, c_void_p, c_void_p, c_int32, i32p, c_void_p]
+                                      c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, sz, i32p, c_void_p]
     lib.wmtp_token_logprobs.restype = c_int32
     lib.wmtp_token_logprobs.argtypes = [c_int32, c_int32, c_int32, c_void_p, i64, c_void_p, c_void_p, c_int32,
                                         c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, i32p, c_void_p]

@@ -3,8 +3,15 @@
 // A sequence of n tokens holds ceil(n / P) pages.  The free list is a stack:
 // with c free pages, R returned and A taken by one call, the returned page of
 // rank r (counted in order of sequence and page) goes to entry c + R - 1 - r,
-// and the taken page of rank a comes from entry c + R - 1 - a.  Both are known
-// from two prefix sums over the sequences, so every page moves on its own.
+// and the taken page of rank a comes from entry c + R - 1 - a.  So the page
+// returned with rank r is the one taken with rank r, and pages of rank R on come from
+// the old entries: with the two prefix sums known every page moves on its own, to
+// the stack and to its new sequence at once, and nothing is read that the call writes.
+//
+// What is moved is small (8 bytes a page, 12 a token); the time is latency.  Up
+// to kFewSeqs sequences take one block and one launch, with a warp's lanes as the
+// sequences; more take a scan of one block, the moves and the map, each over all
+// SMs.
 #pragma once
 
 #include <stdint.h>
@@ -13,8 +20,15 @@
 
 namespace wmtp {
 
-constexpr int kPagesThreads = 1024;
+constexpr int kFewSeqs = 32;
+constexpr int kFewTokens = 4096;
+constexpr int kFewThreads = 512;
+constexpr int kScanThreads = 1024;
+constexpr int kMoveThreads = 256;
+constexpr int kMoveBlocks = 296;
 constexpr int kSlotThreads = 256;
+constexpr int kSlotRows = 4;
+constexpr int kStaged = 2048;  // sequences whose sums are searched in shared memory
 
 struct PagesArgs {
   int32_t* page_table;  // [B][max_pages]
@@ -27,145 +41,263 @@ struct PagesArgs {
   int64_t* slots;
   int32_t* status;
   int B, max_pages, P, num_pages, max_tokens;
+  bool wide;  // positions and slots may be written 16 bytes at a time
+  // between the kernels of many sequences: pages returned and taken before each sequence, and
+  // the stack's height with the returned pages on it
+  int32_t *given, *taken, *top;
 };
 
-// Inclusive prefix sum over the block's threads; *total: the sum of them all.
-__device__ __forceinline__ long long block_scan(long long v, long long* s_warp, long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();  // s_warp free again
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  *total = s_warp[31];
-  return v + (warp > 0 ? s_warp[warp - 1] : 0);
-}
-
 struct SeqChange {
-  int old_len, new_len, hold, want;
+  int old_len, new_len, give, need, grow;
   bool valid;
 };
 
 __device__ __forceinline__ SeqChange seq_change(const PagesArgs& a, int b) {
-  SeqChange c;
-  c.old_len = b < a.B ? a.kv_len[b] : 0;
-  c.new_len = b < a.B ? a.new_len[b] : 0;
+  SeqChange c = {0, 0, 0, 0, 0, false};
+  if (b >= a.B) return c;
+  c.old_len = a.kv_len[b];
+  c.new_len = a.new_len[b];
   const int cap = a.max_pages * a.P;
-  c.valid = b < a.B && c.old_len >= 0 && c.old_len <= cap && c.new_len >= 0 && c.new_len <= cap;
-  c.hold = c.valid ? (c.old_len + a.P - 1) / a.P : 0;
-  c.want = c.valid ? (c.new_len + a.P - 1) / a.P : 0;
+  c.valid = c.old_len >= 0 && c.old_len <= cap && c.new_len >= 0 && c.new_len <= cap;
+  if (!c.valid) {
+    set_status(a.status, kDevLenOob);
+    return c;
+  }
+  const int hold = (c.old_len + a.P - 1) / a.P, want = (c.new_len + a.P - 1) / a.P;
+  c.give = max(hold - want, 0);
+  c.need = max(want - hold, 0);
+  c.grow = max(c.new_len - c.old_len, 0);
   return c;
 }
 
-// One CTA: lengths, page moves, cu.
-__global__ void __launch_bounds__(kPagesThreads) pages_kernel(PagesArgs a) {
-  __shared__ long long s_warp[32];
-  long long total;
+// The first b of [0, n) with end[b] > i.
+__device__ __forceinline__ int first_above(const int32_t* end, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (end[mid] > i)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// Moves the page of rank i: returned, taken, or both.  given, taken: pages
+// before each sequence, [B + 1]; lengths are the new ones.
+__device__ __forceinline__ void move_page(const PagesArgs& a, const int32_t* given, const int32_t* taken, int top, int i) {
+  int32_t page;
+  if (i < given[a.B]) {
+    const int b = first_above(given + 1, a.B, i);
+    const int want = (a.kv_len[b] + a.P - 1) / a.P;
+    int32_t* entry = a.page_table + static_cast<size_t>(b) * a.max_pages + want + (i - given[b]);
+    page = *entry;
+    *entry = -1;
+    if (page < 0 || page >= a.num_pages) set_status(a.status, kDevPageOob);
+    a.free_pages[top - 1 - i] = page;
+  } else {
+    page = a.free_pages[top - 1 - i];
+  }
+  if (i < taken[a.B]) {
+    const int b = first_above(taken + 1, a.B, i);
+    const int hold = (a.kv_len[b] + a.P - 1) / a.P - (taken[b + 1] - taken[b]);
+    a.page_table[static_cast<size_t>(b) * a.max_pages + hold + (i - taken[b])] = page;
+  }
+}
+
+// Row t of the slot map, of sequence b (the first whose tokens end behind it).
+__device__ __forceinline__ void map_slot(const PagesArgs& a, const int32_t* cu, int b, int t, int32_t* pos, int64_t* slot) {
+  *pos = a.kv_len[b] - (cu[b + 1] - t);
+  const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + *pos / a.P];
+  *slot = static_cast<int64_t>(page) * a.P + *pos % a.P;
+  if (page < 0 || page >= a.num_pages) {
+    *slot = -1;
+    set_status(a.status, kDevPageOob);
+  }
+}
+
+// Inclusive prefix sum over a warp's lanes.
+__device__ __forceinline__ long long warp_scan(long long v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+
+// One block: all of it, for up to 32 sequences.
+__global__ void __launch_bounds__(kFewThreads) pages_few_kernel(PagesArgs a) {
+  __shared__ int32_t s_given[kFewSeqs + 1], s_taken[kFewSeqs + 1], s_cu[kFewSeqs + 1], s_top;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+    const int count = *a.free_count;
+    SeqChange c = seq_change(a, tid);
+    const long long given = warp_scan(c.give);
+    const long long top = count + __shfl_sync(0xffffffffu, given, 31);
+    const bool sound = count >= 0 && top <= a.num_pages;
+    if (!sound) {
+      if (tid == 0) set_status(a.status, kDevPool);
+      c = {0, 0, 0, 0, 0, false};
+    }
+    // served in order while pages and rows last: the sums count the refused
+    // sequences too, so whatever grows behind the first one that does not fit is
+    // refused with it
+    const long long need_end = warp_scan(c.need), grow_end = warp_scan(c.grow);
+    const bool served =
+        c.valid && (c.grow == 0 || (need_end <= top && (a.cu == nullptr || grow_end <= a.max_tokens)));
+    if (c.valid && !served) set_status(a.status, kDevPool);
+    const long long taken = warp_scan(served ? c.need : 0), rows = warp_scan(served ? c.grow : 0);
+    if (served) a.kv_len[tid] = c.new_len;
+    s_given[tid + 1] = sound ? static_cast<int32_t>(given) : 0;
+    s_taken[tid + 1] = static_cast<int32_t>(taken);
+    s_cu[tid + 1] = a.cu != nullptr ? static_cast<int32_t>(rows) : 0;
+    if (a.cu != nullptr && tid < a.B) a.cu[tid + 1] = static_cast<int32_t>(rows);
+    if (tid == 31) {
+      if (sound) *a.free_count = static_cast<int32_t>(top - taken);
+      s_top = static_cast<int32_t>(top);
+    }
+    if (tid == 0) {
+      s_given[0] = s_taken[0] = s_cu[0] = 0;
+      if (a.cu != nullptr) a.cu[0] = 0;
+    }
+  }
+  __syncthreads();
+  const int moves = max(s_given[a.B], s_taken[a.B]);
+  for (int i = tid; i < moves; i += kFewThreads) move_page(a, s_given, s_taken, s_top, i);
+  __syncthreads();
+  for (int t = tid; t < a.max_tokens; t += kFewThreads) {
+    int32_t pos = -1;
+    int64_t slot = -1;
+    if (t < s_cu[a.B]) map_slot(a, s_cu, first_above(s_cu + 1, a.B, t), t, &pos, &slot);
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+  }
+}
+
+// Inclusive prefix sums of N values over the block's threads, on top of *carry;
+// *carry: with the block's totals added.
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long (&carry)[N], long long (*s_warp)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = warp_scan(v[n]);
+  __syncthreads();  // s_warp free again
+  if (lane == 31)
+    for (int n = 0; n < N; ++n) s_warp[n][warp] = v[n];
+  __syncthreads();
+  if (warp < N) s_warp[warp][lane] = warp_scan(s_warp[warp][lane]);
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] += carry[n] + (warp > 0 ? s_warp[n][warp - 1] : 0);
+    carry[n] += s_warp[n][31];
+  }
+}
+
+// Many sequences, 1: lengths and prefix sums.
+__global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(PagesArgs a) {
+  __shared__ long long s_warp[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int count = *a.free_count;
-  // 1. pages returned, in order of sequence and page
-  long long released = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
+  long long ends[3] = {0, 0, 0};  // given, needed, grown
+  for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
     const SeqChange c = seq_change(a, b0 + tid);
-    if (b0 + tid < a.B && !c.valid) set_status(a.status, kDevLenOob);
-    released += max(c.hold - c.want, 0);
+    long long v[3] = {c.give, c.need, c.grow};
+    block_scan(v, ends, s_warp);
+    if (b0 + tid < a.B) a.given[b0 + tid + 1] = static_cast<int32_t>(min(v[0], 0x7fffffffLL));
   }
-  block_scan(released, s_warp, &total);
-  released = total;
-  if (count < 0 || count + released > a.num_pages) {
-    if (tid == 0) set_status(a.status, kDevPool);
-    if (a.cu != nullptr)
-      for (int b = tid; b <= a.B; b += kPagesThreads) a.cu[b] = 0;
+  const long long top = count + ends[0];
+  const bool sound = count >= 0 && top <= a.num_pages;
+  if (tid == 0) {
+    a.given[0] = a.taken[0] = 0;
+    if (a.cu != nullptr) a.cu[0] = 0;
+    *a.top = static_cast<int32_t>(top);
+    if (!sound) set_status(a.status, kDevPool);
+  }
+  if (!sound) {
+    for (int b = tid; b < a.B; b += kScanThreads) {
+      a.given[b + 1] = a.taken[b + 1] = 0;
+      if (a.cu != nullptr) a.cu[b + 1] = 0;
+    }
     return;
   }
-  const long long top = count + released;
-  long long before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
-    const SeqChange c = seq_change(a, b0 + tid);
-    const int n = max(c.hold - c.want, 0);
-    const long long first = before + block_scan(n, s_warp, &total) - n;
-    before += total;
-    int32_t* row = a.page_table + static_cast<size_t>(b0 + tid) * a.max_pages;
-    for (int j = 0; j < n; ++j) {
-      const int32_t page = row[c.want + j];
-      if (page < 0 || page >= a.num_pages) set_status(a.status, kDevPageOob);
-      a.free_pages[top - 1 - (first + j)] = page;
-      row[c.want + j] = -1;
-    }
-  }
-  __syncthreads();
-  // 2. pages taken, while they and the rows of the slot map last.  The sums
-  // count the refused sequences too, so whatever grows behind the first one
-  // that does not fit is refused with it
-  long long taken = 0, grown = 0, used_pages = 0, used_rows = 0;
-  if (tid == 0 && a.cu != nullptr) a.cu[0] = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
+  // served in order while pages and rows last: the sums count the refused
+  // sequences too, so whatever grows behind the first one that does not fit is
+  // refused with it
+  long long asked[2] = {0, 0}, used[2] = {0, 0};  // pages, rows
+  for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
     const int b = b0 + tid;
     const SeqChange c = seq_change(a, b);
-    const int grow = c.valid ? max(c.new_len - c.old_len, 0) : 0;
-    const int need = max(c.want - c.hold, 0);
-    const long long need_end = taken + block_scan(need, s_warp, &total);
-    taken += total;
-    const long long grow_end = grown + block_scan(grow, s_warp, &total);
-    grown += total;
-    const bool served = c.valid && (grow == 0 || (need_end <= top && (a.cu == nullptr || grow_end <= a.max_tokens)));
+    long long v[2] = {c.need, c.grow};
+    block_scan(v, asked, s_warp);
+    const bool served = c.valid && (c.grow == 0 || (v[0] <= top && (a.cu == nullptr || v[1] <= a.max_tokens)));
     if (c.valid && !served) set_status(a.status, kDevPool);
-    if (served) {
-      int32_t* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-      for (int j = 0; j < need; ++j) row[c.hold + j] = a.free_pages[top - 1 - (need_end - need + j)];
-      a.kv_len[b] = c.new_len;
+    long long w[2] = {served ? c.need : 0, served ? c.grow : 0};
+    block_scan(w, used, s_warp);
+    if (served) a.kv_len[b] = c.new_len;
+    if (b < a.B) {
+      a.taken[b + 1] = static_cast<int32_t>(w[0]);
+      if (a.cu != nullptr) a.cu[b + 1] = static_cast<int32_t>(w[1]);
     }
-    block_scan(served ? need : 0, s_warp, &total);
-    used_pages += total;
-    const long long rows_end = used_rows + block_scan(served ? grow : 0, s_warp, &total);
-    used_rows += total;
-    if (a.cu != nullptr && b < a.B) a.cu[b + 1] = static_cast<int32_t>(rows_end);
   }
-  if (tid == 0) *a.free_count = static_cast<int32_t>(top - used_pages);
+  if (tid == 0) *a.free_count = static_cast<int32_t>(top - used[0]);
 }
 
-// The slot map, a thread per row: the sequence of row t is the last one with
-// cu[b] <= t; its length now is its old one plus its rows.
+// 2: the pages.
+__global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(PagesArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int32_t s_given[kStaged + 1], s_taken[kStaged + 1];
+  const int moves = max(a.given[a.B], a.taken[a.B]), top = *a.top;
+  if (static_cast<int>(blockIdx.x) * kMoveThreads >= moves) return;
+  const bool staged = a.B <= kStaged;
+  if (staged) {
+    for (int b = threadIdx.x; b <= a.B; b += kMoveThreads) s_given[b] = a.given[b], s_taken[b] = a.taken[b];
+    __syncthreads();
+  }
+  const int32_t *given = staged ? s_given : a.given, *taken = staged ? s_taken : a.taken;
+  for (int i = blockIdx.x * kMoveThreads + threadIdx.x; i < moves; i += kMoveThreads * gridDim.x)
+    move_page(a, given, taken, top, i);
+}
+
+// 3: the slot map, kSlotRows rows to a thread.
 __global__ void __launch_bounds__(kSlotThreads) slots_kernel(PagesArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long t = static_cast<long long>(blockIdx.x) * kSlotThreads + threadIdx.x;
-  if (t >= a.max_tokens) return;
-  int pos = -1;
-  int64_t slot = -1;
-  if (t < a.cu[a.B]) {
-    int lo = 0, hi = a.B - 1;  // the first b with cu[b + 1] > t
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (a.cu[mid + 1] > t)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    pos = a.kv_len[lo] - (a.cu[lo + 1] - static_cast<int>(t));
-    const int page = a.page_table[static_cast<size_t>(lo) * a.max_pages + pos / a.P];
-    if (page >= 0 && page < a.num_pages)
-      slot = static_cast<int64_t>(page) * a.P + pos % a.P;
-    else
-      set_status(a.status, kDevPageOob);
+  const long long first = (static_cast<long long>(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotRows;
+  __shared__ int32_t s_cu[kStaged + 1];
+  const int rows = a.cu[a.B];
+  const bool staged = a.B <= kStaged && first - threadIdx.x * kSlotRows < rows;
+  if (staged) {
+    for (int b = threadIdx.x; b <= a.B; b += kSlotThreads) s_cu[b] = a.cu[b];
+    __syncthreads();
   }
-  a.positions[t] = pos;
-  a.slots[t] = slot;
+  if (first >= a.max_tokens) return;
+  const int32_t* cu = staged ? s_cu : a.cu;
+  const int t0 = static_cast<int>(first), n = min(kSlotRows, a.max_tokens - t0);
+  int32_t pos[kSlotRows];
+  int64_t slot[kSlotRows];
+  int b = t0 < rows ? first_above(cu + 1, a.B, t0) : 0;
+#pragma unroll
+  for (int i = 0; i < kSlotRows; ++i) {
+    pos[i] = -1, slot[i] = -1;
+    if (i >= n || t0 + i >= rows) continue;
+    while (cu[b + 1] <= t0 + i) ++b;
+    map_slot(a, cu, b, t0 + i, &pos[i], &slot[i]);
+  }
+  if (n == kSlotRows && a.wide) {
+    *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    longlong2* to = reinterpret_cast<longlong2*>(a.slots + t0);
+    to[0] = make_longlong2(slot[0], slot[1]);
+    to[1] = make_longlong2(slot[2], slot[3]);
+  } else {
+    for (int i = 0; i < n; ++i) a.positions[t0 + i] = pos[i], a.slots[t0 + i] = slot[i];
+  }
 }
 
 }  // namespace wmtp

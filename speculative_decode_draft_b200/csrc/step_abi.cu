@@ -182,12 +182,20 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
 wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t* page_table, int32_t max_pages,
                               int32_t* kv_len, const int32_t* new_len, int32_t* free_pages, int32_t* free_count,
                               int32_t num_pages, int32_t* cu_tokens, int32_t* positions, int64_t* slots,
-                              int32_t max_tokens, int32_t* status_word, void* stream) {
-  if (params == nullptr || batch < 0 || max_tokens < 0) return WMTP_ERR_INVALID_ARG;
+                              int32_t max_tokens, void* workspace, size_t* workspace_bytes, int32_t* status_word,
+                              void* stream) {
+  if (params == nullptr || batch < 0 || max_tokens < 0 || workspace_bytes == nullptr) return WMTP_ERR_INVALID_ARG;
   if (!supported_page(params->page_size) || batch > kMaxGridYZ) return WMTP_ERR_UNSUPPORTED;
   if (max_pages <= 0 || num_pages <= 0) return WMTP_ERR_INVALID_ARG;
   if (static_cast<long long>(max_pages) * params->page_size > (1LL << 30)) return WMTP_ERR_UNSUPPORTED;
-  const bool map = max_tokens > 0;
+  const bool map = max_tokens > 0, few = batch <= kFewSeqs && max_tokens <= kFewTokens;
+  const size_t need = few ? 0 : align_up((2 * static_cast<size_t>(batch) + 3) * sizeof(int32_t), kWsAlign);
+  if (workspace == nullptr && free_pages == nullptr) {
+    *workspace_bytes = need;
+    return WMTP_OK;
+  }
+  if (*workspace_bytes < need || !aligned(workspace, kWsAlign) || (workspace == nullptr && need > 0))
+    return WMTP_ERR_WORKSPACE;
   if (map != (cu_tokens != nullptr) || map != (positions != nullptr) || map != (slots != nullptr))
     return WMTP_ERR_INVALID_ARG;
   if (free_pages == nullptr || free_count == nullptr || (batch > 0 && (page_table == nullptr || kv_len == nullptr ||
@@ -202,11 +210,15 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
   a.cu = cu_tokens, a.positions = positions, a.slots = slots;
   a.status = status_word;
   a.B = batch, a.max_pages = max_pages, a.P = params->page_size, a.num_pages = num_pages, a.max_tokens = max_tokens;
+  a.wide = aligned(positions, 16) && aligned(slots, 16);
+  a.given = static_cast<int32_t*>(workspace), a.taken = a.given + batch + 1, a.top = a.taken + batch + 1;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  wmtp_status s = launch_plain(true, pages_kernel, dim3(1), dim3(kPagesThreads), st, a);
+  if (few) return launch_plain(true, pages_few_kernel, dim3(1), dim3(kFewThreads), st, a);
+  wmtp_status s = launch_plain(true, pages_scan_kernel, dim3(1), dim3(kScanThreads), st, a);
+  if (s == WMTP_OK) s = launch_plain(true, pages_move_kernel, dim3(kMoveBlocks), dim3(kMoveThreads), st, a);
   if (s != WMTP_OK || !map) return s;
-  return launch_plain(true, slots_kernel, dim3((max_tokens + kSlotThreads - 1) / kSlotThreads), dim3(kSlotThreads), st,
-                      a);
+  return launch_plain(true, slots_kernel, dim3((max_tokens + 1LL * kSlotThreads * kSlotRows - 1) / (kSlotThreads * kSlotRows)),
+                      dim3(kSlotThreads), st, a);
 }
 
 wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, const void* logits, int64_t row_stride,

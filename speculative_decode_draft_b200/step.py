@@ -12,7 +12,7 @@ share nothing.
 
 from __future__ import annotations
 
-import contextlib
+import functools
 import math
 from ctypes import byref, c_size_t
 from dataclasses import dataclass
@@ -21,26 +21,29 @@ from typing import Sequence
 import torch
 
 from . import _lib as L
-from .api import BF16, I32, PagedCache, _need, _ptr
+from .api import BF16, I32, PagedCache, _need, _ptr, params
 
 F32 = torch.float32
 I64 = torch.int64
 _DTYPES = {BF16: L.DTYPE_BF16, torch.float16: L.DTYPE_FP16, F32: L.DTYPE_FP32}
 
 
-def _on(device: torch.device, stream):
-    """Makes ``device`` and ``stream`` current for a call (a no-op where they are)."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+def _run(device: torch.device, stream, body):
+    """``body(raw stream)`` with ``device`` and ``stream`` current."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body(_current_stream(device.index))
+        with torch.cuda.device(device):
+            return body(_current_stream(device.index))
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# torch.cuda.current_stream(i).cuda_stream without the Stream object, where there is such a call
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.device:
@@ -52,9 +55,11 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
 
 
 def _shaped(t: torch.Tensor, dtype, name: str, device, shape) -> None:
-    _need(t, dtype, name, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return
+    _need(t, dtype, name, device)  # says what is wrong
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _check_status(status, device) -> None:
@@ -163,7 +168,7 @@ def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torc
         raise ValueError("q or k is needed")
     dev = _cuda(first, "q" if q is not None else "k")
     dt = first.dtype
-    if dt not in (BF16, F32):
+    if dt is not BF16 and dt is not F32:
         raise TypeError(f"q, k and v must be bf16 or fp32, got {dt}")
     if first.dim() not in (3, 4):
         raise ValueError("q and k must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
@@ -180,42 +185,43 @@ def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torc
         _shaped(slots, I64, "slots", dev, lead)
         if cache is None:
             raise ValueError("slots need a cache")
-        kv = cache.desc()
-        page = (Hkv, p.page_size, D)
-        if (tuple(cache.k_pool.shape[1:]) != page or cache.v_pool.shape != cache.k_pool.shape
-                or cache.k_pool.device != dev or cache.v_pool.device != dev):
-            raise ValueError(f"cache pools must be [num_pages, {Hkv}, {p.page_size}, {D}] on {dev}")
+        kp, vp = cache.k_pool, cache.v_pool
+        pool = (kp.shape[0], Hkv, p.page_size, D)
+        _shaped(kp, BF16, "cache.k_pool", dev, pool)
+        _shaped(vp, BF16, "cache.v_pool", dev, pool)
+        kv = byref(L.PagedKVDesc(kp.data_ptr(), vp.data_ptr(), pool[0], None, 0, None))
     wt = BF16
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             wt = w.dtype
-            if wt not in (BF16, F32):
+            if wt is not BF16 and wt is not F32:
                 raise TypeError(f"{n} must be bf16 or fp32")
             _shaped(w, wt, n, dev, (D,))
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise TypeError("q_weight and k_weight must have one dtype")
     rd = None
     if rope is not None:
-        rd = rope.desc()
         if rope.turn.device != dev:
             raise ValueError(f"rope is on {rope.turn.device}, expected {dev}")
+        rd = byref(rope.desc())
+    if q_out is not None:
+        _shaped(q_out, BF16, "q_out", dev, (*lead, Hq, D))
+    if k_out is not None:
+        _shaped(k_out, BF16, "k_out", dev, (*lead, Hkv, D))
     _check_status(status, dev)
-    with _on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=BF16, device=dev)
-        if k is not None and k_out is None and slots is None:
-            k_out = torch.empty(k.shape, dtype=BF16, device=dev)
-        if q_out is not None:
-            _shaped(q_out, BF16, "q_out", dev, (*lead, Hq, D))
-        if k_out is not None:
-            _shaped(k_out, BF16, "k_out", dev, (*lead, Hkv, D))
-        if tokens == 0:  # empty tensors have no address
-            return q_out, k_out
-        L.check("wmtp_qk_norm_rope", L.load().wmtp_qk_norm_rope(
-            byref(p), None if rd is None else byref(rd), tokens, _DTYPES[dt], *qa, *ka, *va, positions.data_ptr(),
-            _ptr(slots), None if kv is None else byref(kv), _ptr(q_weight), _ptr(k_weight), _DTYPES[wt],
-            weight_offset, eps, _ptr(q_out), _ptr(k_out), _ptr(status), _raw_stream(dev)))
-    return q_out, k_out
+
+    def body(st):
+        qo, ko = q_out, k_out
+        if q is not None and qo is None:
+            qo = torch.empty(q.shape, dtype=BF16, device=dev)
+        if k is not None and ko is None and slots is None:
+            ko = torch.empty(k.shape, dtype=BF16, device=dev)
+        if tokens:  # empty tensors have no address
+            L.check("wmtp_qk_norm_rope", L.load().wmtp_qk_norm_rope(
+                byref(p), rd, tokens, _DTYPES[dt], *qa, *ka, *va, positions.data_ptr(), _ptr(slots), kv,
+                _ptr(q_weight), _ptr(k_weight), _DTYPES[wt], weight_offset, eps, _ptr(qo), _ptr(ko), _ptr(status), st))
+        return qo, ko
+    return _run(dev, stream, body)
 
 
 # ---------------------------------------------------------------- pages
@@ -266,17 +272,32 @@ def pages_resize(p: L.Params, pool: DevicePages, page_table: torch.Tensor, kv_le
     _check_status(status, dev)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    out = None
-    with _on(dev, stream):
+    pages = pool.free.numel()
+    nbytes = _pages_bytes(p.page_size, B, width, pages, max_tokens)
+
+    def body(st):
+        out, ptrs = None, (None, None, None)
         if max_tokens:
             out = SlotMap(torch.empty(B + 1, dtype=I32, device=dev), torch.empty(max_tokens, dtype=I32, device=dev),
                           torch.empty(max_tokens, dtype=I64, device=dev))
-        ptrs = (None, None, None) if out is None else (out.cu_tokens.data_ptr(), out.positions.data_ptr(),
-                                                       out.slots.data_ptr())
+            ptrs = (out.cu_tokens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr())
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         L.check("wmtp_pages_resize", L.load().wmtp_pages_resize(
             byref(p), B, page_table.data_ptr(), width, kv_len.data_ptr(), new_len.data_ptr(), pool.free.data_ptr(),
-            pool.count.data_ptr(), pool.free.numel(), *ptrs, max_tokens, _ptr(status), _raw_stream(dev)))
-    return out
+            pool.count.data_ptr(), pages, *ptrs, max_tokens, _ptr(ws), byref(c_size_t(nbytes)), _ptr(status), st))
+        return out
+    return _run(dev, stream, body)
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_bytes(page_size: int, batch: int, width: int, pages: int, max_tokens: int) -> int:
+    """Scratch of a call of these sizes (the head counts do not matter)."""
+    size = c_size_t(0)
+    anything = 256 if max_tokens else None  # never read: a size query
+    L.check("wmtp_pages_resize", L.load().wmtp_pages_resize(
+        byref(params(1, 1, 64, page_size=page_size)), batch, None, width, None, None, None, None, pages, anything,
+        anything, anything, max_tokens, None, byref(size), None, None))
+    return size.value
 
 
 # ---------------------------------------------------------------- logits
@@ -319,7 +340,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     _check_status(status, dev)
     if top_k < 0:
         raise ValueError("top_k must not be negative")
-    with _on(dev, stream):
+
+    def body(st):
         out = TokenLogprobs(torch.empty(R, n, dtype=F32, device=dev), torch.empty(R, dtype=F32, device=dev),
                             torch.empty(R, dtype=F32, device=dev), None, None)
         if top_k:
@@ -328,8 +350,9 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
         L.check("wmtp_token_logprobs", L.load().wmtp_token_logprobs(
             R, V, _DTYPES[logits.dtype], logits.data_ptr(), _row_stride(logits, 0), _ptr(temperature),
             tokens.data_ptr(), n, top_k, out.logprobs.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
-            _ptr(out.top_logprobs), _ptr(out.top_ids), _ptr(status), _raw_stream(dev)))
-    return out
+            _ptr(out.top_logprobs), _ptr(out.top_ids), _ptr(status), st))
+        return out
+    return _run(dev, stream, body)
 
 
 @dataclass
@@ -369,20 +392,28 @@ def accept_draft(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
     if temperature is not None:
         _shaped(temperature, F32, "temperature", dev, (B,))
     _check_status(status, dev)
-    lib = L.load()
     dt = _DTYPES[target_logits.dtype]
-    with _on(dev, stream):
-        size = c_size_t(0)
-        L.check("wmtp_accept_draft", lib.wmtp_accept_draft(
-            B, n, V, dt, None, 0, 0, None, 0, 0, None, None, None, None, None, None, None, None, byref(size), None,
-            None))
-        ws = torch.empty(max(size.value, 256), dtype=torch.uint8, device=dev)
+    nbytes = _accept_bytes(B, n, V, dt)
+    ds = (0, 0) if draft_logits is None else (_row_stride(draft_logits, 0), _row_stride(draft_logits, 1))
+
+    def body(st):
+        ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=dev)
         out = Accepted(torch.empty(B, n, dtype=I32, device=dev), torch.empty(B, dtype=I32, device=dev),
                        torch.empty(B, n, dtype=F32, device=dev))
-        ds = (0, 0) if draft_logits is None else (_row_stride(draft_logits, 0), _row_stride(draft_logits, 1))
-        L.check("wmtp_accept_draft", lib.wmtp_accept_draft(
+        L.check("wmtp_accept_draft", L.load().wmtp_accept_draft(
             B, n, V, dt, target_logits.data_ptr(), _row_stride(target_logits, 0), _row_stride(target_logits, 1),
             _ptr(draft_logits), *ds, draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_draft),
             _ptr(temperature), out.tokens.data_ptr(), out.count.data_ptr(), out.logprobs.data_ptr(), ws.data_ptr(),
-            byref(size), _ptr(status), _raw_stream(dev)))
-    return out
+            byref(c_size_t(nbytes or 256)), _ptr(status), st))
+        return out
+    return _run(dev, stream, body)
+
+
+@functools.lru_cache(maxsize=256)
+def _accept_bytes(batch: int, num_q: int, vocab: int, dtype: int) -> int:
+    """Scratch of a call of these sizes."""
+    size = c_size_t(0)
+    L.check("wmtp_accept_draft", L.load().wmtp_accept_draft(
+        batch, num_q, vocab, dtype, None, 0, 0, None, 0, 0, None, None, None, None, None, None, None, None,
+        byref(size), None, None))
+    return size.value

@@ -89,10 +89,12 @@ def test_qk_norm_rope_without_tokens_is_a_noop(lib):
 
 
 def _pages(lib, page=64, batch=2, table=A, width=8, kv_len=A, new_len=A, free=A, count=A, pages=8, cu=A, pos=A,
-           slots=A, most=16):
+           slots=A, most=16, ws=A, size=1 << 20):
     p = w.params(16, 2, 256, page_size=page)
-    return lib.wmtp_pages_resize(byref(p), batch, table, width, kv_len, new_len, free, count, pages, cu, pos, slots,
-                                 most, None, None)
+    have = c_size_t(size)
+    code = lib.wmtp_pages_resize(byref(p), batch, table, width, kv_len, new_len, free, count, pages, cu, pos, slots,
+                                 most, ws, byref(have), None, None)
+    return code if ws is not None or free is not None else (code, have.value)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -114,6 +116,10 @@ def _pages(lib, page=64, batch=2, table=A, width=8, kv_len=A, new_len=A, free=A,
     (dict(new_len=None), INVALID),
     (dict(slots=A + 4), INVALID),
     (dict(table=A + 2), INVALID),
+    (dict(ws=A + 16), WORKSPACE),
+    (dict(batch=500, size=8), WORKSPACE),
+    (dict(batch=500, ws=None), WORKSPACE),
+    (dict(most=100000, ws=None), WORKSPACE),
 ])
 def test_pages_resize_refuses(lib, kw, code):
     assert _pages(lib, **kw) == code
@@ -121,6 +127,8 @@ def test_pages_resize_refuses(lib, kw, code):
 
 def test_pages_resize_of_nothing_is_a_noop(lib):
     assert _pages(lib, batch=0, table=None, kv_len=None, new_len=None, cu=None, pos=None, slots=None, most=0) == 0
+    assert _pages(lib, ws=None, free=None) == (0, 0)  # few sequences need no scratch
+    assert _pages(lib, ws=None, free=None, batch=33)[1] > 0
 
 
 def _logprobs(lib, rows=2, vocab=100, dtype=0, logits=A, stride=100, temperature=None, tokens=A, n=1, k=4, lp=A,
