@@ -10,8 +10,9 @@
 //
 // What is moved is small (8 bytes a page, 12 a token); the time is latency.  Up
 // to kFewSeqs sequences take one block and one launch, with a warp's lanes as the
-// sequences; more take a scan of one block, the moves and the map, each over all
-// SMs.
+// sequences.  More take two launches over all SMs: every block works the prefix
+// sums out for itself and moves its share of the pages, and the slot map follows, which
+// also writes what the first kernel's blocks still read, lengths and count.
 #pragma once
 
 #include <stdint.h>
@@ -23,9 +24,9 @@ namespace wmtp {
 constexpr int kFewSeqs = 32;
 constexpr int kFewTokens = 4096;
 constexpr int kFewThreads = 512;
-constexpr int kScanThreads = 1024;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveBlocks = 296;
+constexpr int kMoveThreads = 1024;
+constexpr int kMoveBlocks = 148;
+constexpr int kManyBlocks = 8;  // where the sums do not fit shared memory
 constexpr int kSlotThreads = 256;
 constexpr int kSlotRows = 4;
 constexpr int kStaged = 2048;  // sequences whose sums are searched in shared memory
@@ -42,9 +43,8 @@ struct PagesArgs {
   int32_t* status;
   int B, max_pages, P, num_pages, max_tokens;
   bool wide;  // positions and slots may be written 16 bytes at a time
-  // between the kernels of many sequences: pages returned and taken before each sequence, and
-  // the stack's height with the returned pages on it
-  int32_t *given, *taken, *top;
+  int32_t* after;  // the new free count, then the new lengths: for the second kernel
+  int32_t* sums;   // [kManyBlocks][2][B + 1], above kStaged sequences
 };
 
 struct SeqChange {
@@ -60,7 +60,7 @@ __device__ __forceinline__ SeqChange seq_change(const PagesArgs& a, int b) {
   const int cap = a.max_pages * a.P;
   c.valid = c.old_len >= 0 && c.old_len <= cap && c.new_len >= 0 && c.new_len <= cap;
   if (!c.valid) {
-    set_status(a.status, kDevLenOob);
+    if (blockIdx.x == 0) set_status(a.status, kDevLenOob);
     return c;
   }
   const int hold = (c.old_len + a.P - 1) / a.P, want = (c.new_len + a.P - 1) / a.P;
@@ -84,12 +84,12 @@ __device__ __forceinline__ int first_above(const int32_t* end, int n, int i) {
 }
 
 // Moves the page of rank i: returned, taken, or both.  given, taken: pages
-// before each sequence, [B + 1]; lengths are the new ones.
+// before each sequence, [B + 1].
 __device__ __forceinline__ void move_page(const PagesArgs& a, const int32_t* given, const int32_t* taken, int top, int i) {
   int32_t page;
   if (i < given[a.B]) {
     const int b = first_above(given + 1, a.B, i);
-    const int want = (a.kv_len[b] + a.P - 1) / a.P;
+    const int want = (a.new_len[b] + a.P - 1) / a.P;
     int32_t* entry = a.page_table + static_cast<size_t>(b) * a.max_pages + want + (i - given[b]);
     page = *entry;
     *entry = -1;
@@ -100,14 +100,14 @@ __device__ __forceinline__ void move_page(const PagesArgs& a, const int32_t* giv
   }
   if (i < taken[a.B]) {
     const int b = first_above(taken + 1, a.B, i);
-    const int hold = (a.kv_len[b] + a.P - 1) / a.P - (taken[b + 1] - taken[b]);
+    const int hold = (a.kv_len[b] + a.P - 1) / a.P;  // the old length
     a.page_table[static_cast<size_t>(b) * a.max_pages + hold + (i - taken[b])] = page;
   }
 }
 
 // Row t of the slot map, of sequence b (the first whose tokens end behind it).
 __device__ __forceinline__ void map_slot(const PagesArgs& a, const int32_t* cu, int b, int t, int32_t* pos, int64_t* slot) {
-  *pos = a.kv_len[b] - (cu[b + 1] - t);
+  *pos = a.new_len[b] - (cu[b + 1] - t);
   const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + *pos / a.P];
   *slot = static_cast<int64_t>(page) * a.P + *pos % a.P;
   if (page < 0 || page >= a.num_pages) {
@@ -129,6 +129,7 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // One block: all of it, for up to 32 sequences.
 __global__ void __launch_bounds__(kFewThreads) pages_few_kernel(PagesArgs a) {
   __shared__ int32_t s_given[kFewSeqs + 1], s_taken[kFewSeqs + 1], s_cu[kFewSeqs + 1], s_top;
+  __shared__ bool s_served[kFewSeqs];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kFewThreads) pages_few_kernel(PagesArgs a) {
         c.valid && (c.grow == 0 || (need_end <= top && (a.cu == nullptr || grow_end <= a.max_tokens)));
     if (c.valid && !served) set_status(a.status, kDevPool);
     const long long taken = warp_scan(served ? c.need : 0), rows = warp_scan(served ? c.grow : 0);
-    if (served) a.kv_len[tid] = c.new_len;
+    s_served[tid] = served;
     s_given[tid + 1] = sound ? static_cast<int32_t>(given) : 0;
     s_taken[tid + 1] = static_cast<int32_t>(taken);
     s_cu[tid + 1] = a.cu != nullptr ? static_cast<int32_t>(rows) : 0;
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kFewThreads) pages_few_kernel(PagesArgs a) {
     a.positions[t] = pos;
     a.slots[t] = slot;
   }
+  if (tid < a.B && s_served[tid]) a.kv_len[tid] = a.new_len[tid];  // read as the old one by the moves
 }
 
 // Inclusive prefix sums of N values over the block's threads, on top of *carry;
@@ -197,80 +199,75 @@ __device__ __forceinline__ void block_scan(long long (&v)[N], long long (&carry)
   }
 }
 
-// Many sequences, 1: lengths and prefix sums.
-__global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(PagesArgs a) {
+// Many sequences, 1: prefix sums, by every block for itself, and the pages.
+__global__ void __launch_bounds__(kMoveThreads) pages_kernel(PagesArgs a) {
   __shared__ long long s_warp[3][32];
+  __shared__ int32_t s_given[kStaged + 1], s_taken[kStaged + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
+  const bool writes = blockIdx.x == 0;
+  int32_t* given = a.B <= kStaged ? s_given : a.sums + static_cast<size_t>(blockIdx.x) * 2 * (a.B + 1);
+  int32_t* taken = a.B <= kStaged ? s_taken : given + a.B + 1;
   const int count = *a.free_count;
-  long long ends[3] = {0, 0, 0};  // given, needed, grown
-  for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
-    const SeqChange c = seq_change(a, b0 + tid);
-    long long v[3] = {c.give, c.need, c.grow};
+  long long ends[3] = {0, 0, 0}, v[3];  // given, needed, grown
+  SeqChange c;
+  for (int b0 = 0; b0 < a.B; b0 += kMoveThreads) {
+    c = seq_change(a, b0 + tid);
+    v[0] = c.give, v[1] = c.need, v[2] = c.grow;
     block_scan(v, ends, s_warp);
-    if (b0 + tid < a.B) a.given[b0 + tid + 1] = static_cast<int32_t>(min(v[0], 0x7fffffffLL));
+    if (b0 + tid < a.B) given[b0 + tid + 1] = static_cast<int32_t>(min(v[0], 0x7fffffffLL));
   }
   const long long top = count + ends[0];
   const bool sound = count >= 0 && top <= a.num_pages;
-  if (tid == 0) {
-    a.given[0] = a.taken[0] = 0;
-    if (a.cu != nullptr) a.cu[0] = 0;
-    *a.top = static_cast<int32_t>(top);
-    if (!sound) set_status(a.status, kDevPool);
-  }
-  if (!sound) {
-    for (int b = tid; b < a.B; b += kScanThreads) {
-      a.given[b + 1] = a.taken[b + 1] = 0;
-      if (a.cu != nullptr) a.cu[b + 1] = 0;
-    }
-    return;
-  }
   // served in order while pages and rows last: the sums count the refused
   // sequences too, so whatever grows behind the first one that does not fit is
   // refused with it
-  long long asked[2] = {0, 0}, used[2] = {0, 0};  // pages, rows
-  for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
+  long long again[3] = {0, 0, 0}, used[2] = {0, 0};  // pages, rows
+  for (int b0 = 0; b0 < a.B; b0 += kMoveThreads) {
     const int b = b0 + tid;
-    const SeqChange c = seq_change(a, b);
-    long long v[2] = {c.need, c.grow};
-    block_scan(v, asked, s_warp);
-    const bool served = c.valid && (c.grow == 0 || (v[0] <= top && (a.cu == nullptr || v[1] <= a.max_tokens)));
-    if (c.valid && !served) set_status(a.status, kDevPool);
+    if (a.B > kMoveThreads) {  // else the only round's sums are still there
+      c = seq_change(a, b);
+      v[0] = c.give, v[1] = c.need, v[2] = c.grow;
+      block_scan(v, again, s_warp);
+    }
+    const bool served =
+        sound && c.valid && (c.grow == 0 || (v[1] <= top && (a.cu == nullptr || v[2] <= a.max_tokens)));
     long long w[2] = {served ? c.need : 0, served ? c.grow : 0};
     block_scan(w, used, s_warp);
-    if (served) a.kv_len[b] = c.new_len;
     if (b < a.B) {
-      a.taken[b + 1] = static_cast<int32_t>(w[0]);
-      if (a.cu != nullptr) a.cu[b + 1] = static_cast<int32_t>(w[1]);
+      taken[b + 1] = static_cast<int32_t>(w[0]);
+      if (writes) {
+        if (sound && c.valid && !served) set_status(a.status, kDevPool);
+        a.after[1 + b] = served ? c.new_len : c.old_len;
+        if (a.cu != nullptr) a.cu[b + 1] = static_cast<int32_t>(w[1]);
+      }
     }
   }
-  if (tid == 0) *a.free_count = static_cast<int32_t>(top - used[0]);
-}
-
-// 2: the pages.
-__global__ void __launch_bounds__(kMoveThreads) pages_move_kernel(PagesArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int32_t s_given[kStaged + 1], s_taken[kStaged + 1];
-  const int moves = max(a.given[a.B], a.taken[a.B]), top = *a.top;
-  if (static_cast<int>(blockIdx.x) * kMoveThreads >= moves) return;
-  const bool staged = a.B <= kStaged;
-  if (staged) {
-    for (int b = threadIdx.x; b <= a.B; b += kMoveThreads) s_given[b] = a.given[b], s_taken[b] = a.taken[b];
-    __syncthreads();
+  if (tid == 0) {
+    given[0] = taken[0] = 0;
+    if (writes) {
+      a.after[0] = sound ? static_cast<int32_t>(top - used[0]) : count;
+      if (a.cu != nullptr) a.cu[0] = 0;
+      if (!sound) set_status(a.status, kDevPool);
+    }
   }
-  const int32_t *given = staged ? s_given : a.given, *taken = staged ? s_taken : a.taken;
-  for (int i = blockIdx.x * kMoveThreads + threadIdx.x; i < moves; i += kMoveThreads * gridDim.x)
-    move_page(a, given, taken, top, i);
+  if (!sound) return;
+  __syncthreads();
+  const int moves = static_cast<int>(max(ends[0], used[0]));
+  for (int i = blockIdx.x * kMoveThreads + tid; i < moves; i += kMoveThreads * gridDim.x)
+    move_page(a, given, taken, static_cast<int>(top), i);
 }
 
-// 3: the slot map, kSlotRows rows to a thread.
+// 2: lengths and count, and the slot map, kSlotRows rows to a thread.
 __global__ void __launch_bounds__(kSlotThreads) slots_kernel(PagesArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long first = (static_cast<long long>(blockIdx.x) * kSlotThreads + threadIdx.x) * kSlotRows;
   __shared__ int32_t s_cu[kStaged + 1];
+  for (int b = blockIdx.x * kSlotThreads + threadIdx.x; b < a.B; b += kSlotThreads * gridDim.x) a.kv_len[b] = a.after[1 + b];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_count = a.after[0];
+  if (a.max_tokens == 0) return;
   const int rows = a.cu[a.B];
   const bool staged = a.B <= kStaged && first - threadIdx.x * kSlotRows < rows;
   if (staged) {

@@ -189,7 +189,9 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
   if (max_pages <= 0 || num_pages <= 0) return WMTP_ERR_INVALID_ARG;
   if (static_cast<long long>(max_pages) * params->page_size > (1LL << 30)) return WMTP_ERR_UNSUPPORTED;
   const bool map = max_tokens > 0, few = batch <= kFewSeqs && max_tokens <= kFewTokens;
-  const size_t need = few ? 0 : align_up((2 * static_cast<size_t>(batch) + 3) * sizeof(int32_t), kWsAlign);
+  const bool staged = batch <= kStaged;
+  const size_t seqs = static_cast<size_t>(batch) + 1;
+  const size_t need = few ? 0 : align_up((staged ? seqs : (1 + 2 * kManyBlocks) * seqs) * sizeof(int32_t), kWsAlign);
   if (workspace == nullptr && free_pages == nullptr) {
     *workspace_bytes = need;
     return WMTP_OK;
@@ -211,14 +213,14 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
   a.status = status_word;
   a.B = batch, a.max_pages = max_pages, a.P = params->page_size, a.num_pages = num_pages, a.max_tokens = max_tokens;
   a.wide = aligned(positions, 16) && aligned(slots, 16);
-  a.given = static_cast<int32_t*>(workspace), a.taken = a.given + batch + 1, a.top = a.taken + batch + 1;
+  a.after = static_cast<int32_t*>(workspace), a.sums = a.after + seqs;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) return launch_plain(true, pages_few_kernel, dim3(1), dim3(kFewThreads), st, a);
-  wmtp_status s = launch_plain(true, pages_scan_kernel, dim3(1), dim3(kScanThreads), st, a);
-  if (s == WMTP_OK) s = launch_plain(true, pages_move_kernel, dim3(kMoveBlocks), dim3(kMoveThreads), st, a);
-  if (s != WMTP_OK || !map) return s;
-  return launch_plain(true, slots_kernel, dim3((max_tokens + 1LL * kSlotThreads * kSlotRows - 1) / (kSlotThreads * kSlotRows)),
-                      dim3(kSlotThreads), st, a);
+  const wmtp_status s =
+      launch_plain(true, pages_kernel, dim3(staged ? kMoveBlocks : kManyBlocks), dim3(kMoveThreads), st, a);
+  if (s != WMTP_OK) return s;
+  const long long blocks = (max_tokens + 1LL * kSlotThreads * kSlotRows - 1) / (kSlotThreads * kSlotRows);
+  return launch_plain(true, slots_kernel, dim3(static_cast<unsigned>(blocks > 0 ? blocks : 1)), dim3(kSlotThreads), st, a);
 }
 
 wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, const void* logits, int64_t row_stride,

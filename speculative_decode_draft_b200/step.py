@@ -28,43 +28,40 @@ I64 = torch.int64
 _DTYPES = {BF16: L.DTYPE_BF16, torch.float16: L.DTYPE_FP16, F32: L.DTYPE_FP32}
 
 
-def _run(device: torch.device, stream, body):
-    """``body(raw stream)`` with ``device`` and ``stream`` current."""
-    if stream is None:
-        if device.index == torch.cuda.current_device():
-            return body(_current_stream(device.index))
-        with torch.cuda.device(device):
-            return body(_current_stream(device.index))
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
-
-
 # torch.cuda.current_stream(i).cuda_stream without the Stream object, where there is such a call
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _cuda(t: torch.Tensor, name: str) -> torch.device:
+def _elsewhere(index: int, stream):
+    """The context that makes device ``index`` and ``stream`` current, None where they are."""
+    if stream is None:
+        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
+    return torch.cuda.stream(stream)
+
+
+def _cuda(t: torch.Tensor, name: str) -> int:
+    """The tensor's device index."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _shaped(t: torch.Tensor, dtype, name: str, device, shape) -> None:
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+def _shaped(t: torch.Tensor, dtype, name: str, index: int, shape) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
         return
-    _need(t, dtype, name, device)  # says what is wrong
+    _need(t, dtype, name, torch.device("cuda", index))  # says what is wrong
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _check_status(status, device) -> None:
+def _check_status(status, index: int) -> None:
     if status is not None:
-        _need(status, I32, "status", device)
+        _need(status, I32, "status", torch.device("cuda", index))
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -129,24 +126,28 @@ class Rope:
         return L.RopeDesc(self.turn.data_ptr(), 2 * self.turn.numel(), int(bool(self.interleaved)), self.factor)
 
 
-def _heads(t: torch.Tensor, name: str, device, dtype, lead, heads: int, dim: int):
+def _heads(t: torch.Tensor, name: str, index: int, dtype, lead, heads: int, dim: int):
     """(pointer, token stride, head stride) of a ``[..., heads, dim]`` view with one token stride."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (*lead, heads, dim):
         raise ValueError(f"{name} must be {[*lead, heads, dim]}, got {list(t.shape)}")
     st = t.stride()
-    if t.numel() == 0:
-        return t.data_ptr(), 0, 0
     if dim > 1 and st[-1] != 1:
         raise ValueError(f"{name}: the elements of a head must be next to one another")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
-        raise ValueError(f"{name}: tokens must be evenly spaced")
-    token = st[0] if len(lead) == 1 or lead[1] == 1 else st[1]
-    # strides of axes with one entry say nothing
-    return t.data_ptr(), token if math.prod(lead) > 1 else 0, st[-2] if heads > 1 else 0
+    token = st[0]  # strides of axes with one entry say nothing
+    if len(lead) == 1:
+        if lead[0] <= 1:
+            token = 0
+    elif lead[1] > 1:
+        if lead[0] > 1 and st[0] != lead[1] * st[1]:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+        token = st[1]
+    elif lead[0] <= 1:
+        token = 0
+    return t.data_ptr(), token, st[-2] if heads > 1 else 0
 
 
 def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torch.Tensor | None,
@@ -167,6 +168,12 @@ def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torc
     if first is None:
         raise ValueError("q or k is needed")
     dev = _cuda(first, "q" if q is not None else "k")
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return qk_norm_rope(p, rope, q, k, v, positions, slots=slots, cache=cache, q_weight=q_weight,
+                                k_weight=k_weight, eps=eps, weight_offset=weight_offset, q_out=q_out, k_out=k_out,
+                                status=status)
     dt = first.dtype
     if dt is not BF16 and dt is not F32:
         raise TypeError(f"q, k and v must be bf16 or fp32, got {dt}")
@@ -201,27 +208,24 @@ def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torc
         raise TypeError("q_weight and k_weight must have one dtype")
     rd = None
     if rope is not None:
-        if rope.turn.device != dev:
-            raise ValueError(f"rope is on {rope.turn.device}, expected {dev}")
+        if rope.turn.get_device() != dev:
+            raise ValueError(f"rope is on {rope.turn.device}, expected cuda:{dev}")
         rd = byref(rope.desc())
     if q_out is not None:
         _shaped(q_out, BF16, "q_out", dev, (*lead, Hq, D))
+    elif q is not None:
+        q_out = torch.empty(q.shape, dtype=BF16, device=q.device)
     if k_out is not None:
         _shaped(k_out, BF16, "k_out", dev, (*lead, Hkv, D))
+    elif k is not None and slots is None:
+        k_out = torch.empty(k.shape, dtype=BF16, device=k.device)
     _check_status(status, dev)
-
-    def body(st):
-        qo, ko = q_out, k_out
-        if q is not None and qo is None:
-            qo = torch.empty(q.shape, dtype=BF16, device=dev)
-        if k is not None and ko is None and slots is None:
-            ko = torch.empty(k.shape, dtype=BF16, device=dev)
-        if tokens:  # empty tensors have no address
-            L.check("wmtp_qk_norm_rope", L.load().wmtp_qk_norm_rope(
-                byref(p), rd, tokens, _DTYPES[dt], *qa, *ka, *va, positions.data_ptr(), _ptr(slots), kv,
-                _ptr(q_weight), _ptr(k_weight), _DTYPES[wt], weight_offset, eps, _ptr(qo), _ptr(ko), _ptr(status), st))
-        return qo, ko
-    return _run(dev, stream, body)
+    if tokens:  # empty tensors have no address
+        L.check("wmtp_qk_norm_rope", L.load().wmtp_qk_norm_rope(
+            byref(p), rd, tokens, _DTYPES[dt], *qa, *ka, *va, positions.data_ptr(), _ptr(slots), kv, _ptr(q_weight),
+            _ptr(k_weight), _DTYPES[wt], weight_offset, eps, _ptr(q_out), _ptr(k_out), _ptr(status),
+            _current_stream(dev)))
+    return q_out, k_out
 
 
 # ---------------------------------------------------------------- pages
@@ -261,32 +265,35 @@ def pages_resize(p: L.Params, pool: DevicePages, page_table: torch.Tensor, kv_le
     cache slots are returned, as ``qk_norm_rope`` takes them.
     """
     dev = _cuda(page_table, "page_table")
-    _need(page_table, I32, "page_table", dev)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return pages_resize(p, pool, page_table, kv_len, new_len, max_tokens=max_tokens, status=status)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, max_pages]")
     B, width = page_table.shape
+    _shaped(page_table, I32, "page_table", dev, (B, width))
     _shaped(kv_len, I32, "kv_len", dev, (B,))
     _shaped(new_len, I32, "new_len", dev, (B,))
-    _need(pool.free, I32, "pool.free", dev)
+    pages = pool.free.numel()
+    _shaped(pool.free, I32, "pool.free", dev, (pages,))
     _shaped(pool.count, I32, "pool.count", dev, (1,))
     _check_status(status, dev)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    pages = pool.free.numel()
+    device = page_table.device
+    out, ptrs = None, (None, None, None)
+    if max_tokens:
+        out = SlotMap(torch.empty(B + 1, dtype=I32, device=device), torch.empty(max_tokens, dtype=I32, device=device),
+                      torch.empty(max_tokens, dtype=I64, device=device))
+        ptrs = (out.cu_tokens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr())
     nbytes = _pages_bytes(p.page_size, B, width, pages, max_tokens)
-
-    def body(st):
-        out, ptrs = None, (None, None, None)
-        if max_tokens:
-            out = SlotMap(torch.empty(B + 1, dtype=I32, device=dev), torch.empty(max_tokens, dtype=I32, device=dev),
-                          torch.empty(max_tokens, dtype=I64, device=dev))
-            ptrs = (out.cu_tokens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr())
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        L.check("wmtp_pages_resize", L.load().wmtp_pages_resize(
-            byref(p), B, page_table.data_ptr(), width, kv_len.data_ptr(), new_len.data_ptr(), pool.free.data_ptr(),
-            pool.count.data_ptr(), pages, *ptrs, max_tokens, _ptr(ws), byref(c_size_t(nbytes)), _ptr(status), st))
-        return out
-    return _run(dev, stream, body)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    L.check("wmtp_pages_resize", L.load().wmtp_pages_resize(
+        byref(p), B, page_table.data_ptr(), width, kv_len.data_ptr(), new_len.data_ptr(), pool.free.data_ptr(),
+        pool.count.data_ptr(), pages, *ptrs, max_tokens, _ptr(ws), byref(c_size_t(nbytes)), _ptr(status),
+        _current_stream(dev)))
+    return out
 
 
 @functools.lru_cache(maxsize=256)
@@ -329,6 +336,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     ``logits``: bf16, fp16 or fp32, rows any stride apart.  ``temperature`` fp32 ``[rows]``, above 0.
     """
     dev = _cuda(logits, "logits")
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return token_logprobs(logits, tokens, top_k=top_k, temperature=temperature, status=status)
     _logits_ok(logits, "logits")
     if logits.dim() != 2 or tokens.dim() != 2:
         raise ValueError("logits must be [rows, vocab] and tokens [rows, n]")
@@ -340,19 +351,19 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     _check_status(status, dev)
     if top_k < 0:
         raise ValueError("top_k must not be negative")
-
-    def body(st):
-        out = TokenLogprobs(torch.empty(R, n, dtype=F32, device=dev), torch.empty(R, dtype=F32, device=dev),
-                            torch.empty(R, dtype=F32, device=dev), None, None)
-        if top_k:
-            out.top_logprobs = torch.empty(R, top_k, dtype=F32, device=dev)
-            out.top_ids = torch.empty(R, top_k, dtype=I32, device=dev)
-        L.check("wmtp_token_logprobs", L.load().wmtp_token_logprobs(
-            R, V, _DTYPES[logits.dtype], logits.data_ptr(), _row_stride(logits, 0), _ptr(temperature),
-            tokens.data_ptr(), n, top_k, out.logprobs.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
-            _ptr(out.top_logprobs), _ptr(out.top_ids), _ptr(status), st))
-        return out
-    return _run(dev, stream, body)
+    device = logits.device
+    logprobs = torch.empty(R, n, dtype=F32, device=device)
+    entropy = torch.empty(R, dtype=F32, device=device)
+    lse = torch.empty(R, dtype=F32, device=device)
+    top_logprobs = top_ids = None
+    if top_k:
+        top_logprobs = torch.empty(R, top_k, dtype=F32, device=device)
+        top_ids = torch.empty(R, top_k, dtype=I32, device=device)
+    L.check("wmtp_token_logprobs", L.load().wmtp_token_logprobs(
+        R, V, _DTYPES[logits.dtype], logits.data_ptr(), _row_stride(logits, 0), _ptr(temperature), tokens.data_ptr(),
+        n, top_k, logprobs.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(top_logprobs), _ptr(top_ids),
+        _ptr(status), _current_stream(dev)))
+    return TokenLogprobs(logprobs, entropy, lse, top_logprobs, top_ids)
 
 
 @dataclass
@@ -373,6 +384,11 @@ def accept_draft(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
     were drafted, at most gamma.  ``temperature`` fp32 ``[B]``; 0 is greedy.
     """
     dev = _cuda(target_logits, "target_logits")
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return accept_draft(target_logits, draft_tokens, uniforms, draft_logits=draft_logits, num_draft=num_draft,
+                                temperature=temperature, status=status)
     _logits_ok(target_logits, "target_logits")
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [batch, gamma + 1, vocab]")
@@ -381,32 +397,31 @@ def accept_draft(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
         raise ValueError("target_logits needs a row for the token that follows")
     _shaped(draft_tokens, I32, "draft_tokens", dev, (B, n - 1))
     _shaped(uniforms, F32, "uniforms", dev, (B, n))
+    ds = (0, 0)
     if draft_logits is not None:
         _logits_ok(draft_logits, "draft_logits")
-        if draft_logits.device != dev or draft_logits.dtype != target_logits.dtype:
+        if draft_logits.get_device() != dev or draft_logits.dtype is not target_logits.dtype:
             raise TypeError("draft_logits must have the device and dtype of target_logits")
         if draft_logits.shape != (B, n - 1, V):
             raise ValueError(f"draft_logits must be {[B, n - 1, V]}, got {list(draft_logits.shape)}")
+        ds = (_row_stride(draft_logits, 0), _row_stride(draft_logits, 1))
     if num_draft is not None:
         _shaped(num_draft, I32, "num_draft", dev, (B,))
     if temperature is not None:
         _shaped(temperature, F32, "temperature", dev, (B,))
     _check_status(status, dev)
-    dt = _DTYPES[target_logits.dtype]
+    device, dt = target_logits.device, _DTYPES[target_logits.dtype]
     nbytes = _accept_bytes(B, n, V, dt)
-    ds = (0, 0) if draft_logits is None else (_row_stride(draft_logits, 0), _row_stride(draft_logits, 1))
-
-    def body(st):
-        ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=dev)
-        out = Accepted(torch.empty(B, n, dtype=I32, device=dev), torch.empty(B, dtype=I32, device=dev),
-                       torch.empty(B, n, dtype=F32, device=dev))
-        L.check("wmtp_accept_draft", L.load().wmtp_accept_draft(
-            B, n, V, dt, target_logits.data_ptr(), _row_stride(target_logits, 0), _row_stride(target_logits, 1),
-            _ptr(draft_logits), *ds, draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_draft),
-            _ptr(temperature), out.tokens.data_ptr(), out.count.data_ptr(), out.logprobs.data_ptr(), ws.data_ptr(),
-            byref(c_size_t(nbytes or 256)), _ptr(status), st))
-        return out
-    return _run(dev, stream, body)
+    ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=device)
+    tokens = torch.empty(B, n, dtype=I32, device=device)
+    count = torch.empty(B, dtype=I32, device=device)
+    logprobs = torch.empty(B, n, dtype=F32, device=device)
+    L.check("wmtp_accept_draft", L.load().wmtp_accept_draft(
+        B, n, V, dt, target_logits.data_ptr(), _row_stride(target_logits, 0), _row_stride(target_logits, 1),
+        _ptr(draft_logits), *ds, draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_draft), _ptr(temperature),
+        tokens.data_ptr(), count.data_ptr(), logprobs.data_ptr(), ws.data_ptr(), byref(c_size_t(nbytes or 256)),
+        _ptr(status), _current_stream(dev)))
+    return Accepted(tokens, count, logprobs)
 
 
 @functools.lru_cache(maxsize=256)
