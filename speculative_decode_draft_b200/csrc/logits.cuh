@@ -252,7 +252,7 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
   const float slack = 8.f / c;
   const uint64_t c2 = pack2(c, c);
   uint64_t s2 = 0, a2 = 0, minus_a2 = 0;
-  float raise_at = -INFINITY;
+  float raise_at = kLowest;  // what lies below counts as masked here
   auto sums = [&]() {
     float s0, s1, a0, a1;
     unpack2(s2, s0, s1);
@@ -274,8 +274,10 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
       const float by = __fmul_rn(z.r.m, c) - __fmul_rn(top, c), f = exp2_fast(by);
       z.r.m = top;
       raise_at = top + slack;
-      s2 = pack2(o.x == 0.f ? 0.f : f * o.x, 0.f);
-      a2 = pack2(o.x == 0.f ? 0.f : f * (o.y + by * o.x), 0.f);
+      // a run of -1e10, say, has lost all digits against its anchor, and may have overflowed
+      const bool gone = o.x == 0.f || (f == 0.f && o.x == o.x);
+      s2 = pack2(gone ? 0.f : f * o.x, 0.f);
+      a2 = pack2(gone ? 0.f : f * (o.y + by * o.x), 0.f);
       minus_a2 = pack2(__fmul_rn(-top, c), __fmul_rn(-top, c));
     }
 #pragma unroll
@@ -332,7 +334,7 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
   z.r.s = o.x, z.r.a = o.y;
   if (z.best == -INFINITY) {  // masked: no weight, but NaN stays
     z.r.m = -FLT_MAX;
-  } else if (fabsf(z.r.m) < 1e29f && fabsf(z.r.m * c) < 1e6f && c > 1e-20f && c < 1e7f) {
+  } else if (z.best > -1e29f && fabsf(z.r.m) < 1e29f && fabsf(z.r.m * c) < 1e6f && c > 1e-20f && c < 1e7f) {
     const float low = fmaf(z.r.m, c, -__fmul_rn(z.r.m, c)), f = exp2f(-low);
     z.r.s = f * o.x;
     z.r.a = f * (o.y - low * o.x) / c;

@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(kMoveThreads) pages_kernel(PagesArgs a) {
   }
   if (!sound) return;
   __syncthreads();
-  const int moves = static_cast<int>(max(ends[0], used[0]));
-  for (int i = blockIdx.x * kMoveThreads + tid; i < moves; i += kMoveThreads * gridDim.x)
-    move_page(a, given, taken, static_cast<int>(top), i);
+  const long long moves = max(ends[0], used[0]);
+  for (long long i = static_cast<long long>(blockIdx.x) * kMoveThreads + tid; i < moves; i += kMoveThreads * gridDim.x)
+    move_page(a, given, taken, static_cast<int>(top), static_cast<int>(i));
 }
 
 // 2: lengths and count, and the slot map, kSlotRows rows to a thread.

@@ -62,7 +62,7 @@ def _check_rows(x, tokens, top_k, temperature, r):
             def close(got, ids):
                 for a, j in zip(got, ids):
                     want = ref[j] if 0 <= j < len(row) else -np.inf
-                    if want == -np.inf:
+                    if want <= -2.0 ** 128:  # beyond fp32, which rounds it to -inf
                         assert a == -np.inf
                     else:
                         assert abs(a - want) <= tol + 3 * U * abs(y[j]) + U * abs(want), (i, j, a, want)
@@ -149,6 +149,54 @@ def test_logprob_masked_and_extreme_rows(cuda_device):
     assert lp[3, 2] == 0 and lp[3, 0] == NEG and r.top_ids[3].tolist() == [9, -1, -1]
     assert abs(float(lp[4, 0]) + np.log(V - 1)) < 1e-5 and lp[4, 3] == NEG
     _check_rows(x[5:], tokens[5:], 3, None, w.token_logprobs(x[5:], tokens[5:], top_k=3))
+
+
+@pytest.mark.parametrize("t", [1e-30, 1e-6, 0.01, 100.0, 1e6, 1e30])
+@pytest.mark.parametrize("masked", [False, True])
+def test_logprob_extreme_temperatures(cuda_device, t, masked):
+    x = torch.randn(4, 5001, generator=_gen(20), device=DEV)
+    if masked:
+        x[:, ::3] = NEG
+        x[3, 1:] = NEG
+        x[3, 0] = 1.0
+    tokens = torch.tensor([[0, 1, 5000]] * 4, dtype=torch.int32, device=DEV)
+    temps = torch.full((4,), t, device=DEV)
+    status = w.new_status(DEV)
+    r = w.token_logprobs(x, tokens, top_k=4, temperature=temps, status=status)
+    assert int(status.item()) == 0
+    if t == 1e-30:  # all but the largest underflow; the others' log probabilities pass fp32 or not
+        assert (r.entropy == 0).all() and (r.top_logprobs[:, 0] == 0).all()
+        assert r.top_ids.tolist() == [oracle.top_tokens(row, 4) for row in f64(x)]
+        return
+    _check_rows(x, tokens, 4, temps, r)
+
+
+@pytest.mark.parametrize("dtype,shift", [("fp32", 3e5), ("fp32", -3e5), ("fp32", 1e7), ("fp32", 1e20), ("fp32", -1e35),
+                                         ("fp16", 6e4), ("fp16", -6e4), ("bf16", 3e5), ("bf16", -1e38), ("bf16", 2e38)])
+def test_logprob_large_logits(cuda_device, dtype, shift):
+    """Far from 0: differences keep their digits."""
+    g = _gen(21)
+    step = abs(shift) * torch.finfo(DT[dtype]).eps
+    x = (shift + torch.randint(-6, 7, (3, 4007), generator=g, device=DEV) * step).to(DT[dtype])
+    x[1, 7:900] = NEG
+    t = torch.full((3,), max(1.0, step), device=DEV)
+    tokens = torch.randint(0, 4007, (3, 3), generator=g, device=DEV).int()
+    status = w.new_status(DEV)
+    r = w.token_logprobs(x, tokens, top_k=3, temperature=t, status=status)
+    assert int(status.item()) == 0
+    _check_rows(x, tokens, 3, t, r)
+
+
+def test_logprob_offsets_beyond_32_bits(cuda_device):
+    R, V = 17000, 131072  # 2.2e9 logits
+    x = torch.zeros(R, V, dtype=torch.bfloat16, device=DEV)
+    last = torch.randn(3, V, generator=_gen(22), device=DEV).bfloat16()
+    x[-3:] = last
+    tokens = torch.full((R, 1), 77, dtype=torch.int32, device=DEV)
+    r = w.token_logprobs(x, tokens, top_k=2)
+    assert (r.logprobs[:-3] + np.log(V)).abs().max() < 1e-5 and (r.top_ids[:-3] == torch.tensor([0, 1], device=DEV)).all()
+    _check_rows(last, tokens[-3:], 2, None, w.TokenLogprobs(r.logprobs[-3:], r.entropy[-3:], r.lse[-3:],
+                                                            r.top_logprobs[-3:], r.top_ids[-3:]))
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
@@ -343,6 +391,39 @@ def test_accept_bad_rows_lengths_and_ids(cuda_device):
     status.zero_()
     r = w.accept_draft(x, tokens, u, num_draft=torch.zeros_like(num), status=status)
     assert int(status.item()) == 0 and r.count.tolist() == [1] * B and (r.tokens[:, 0] == 5).all()
+
+
+def test_accept_same_distributions_accept_everything(cuda_device):
+    x = torch.randn(50, 4, 3001, generator=_gen(30), device=DEV).half()
+    tokens = torch.randint(0, 3001, (50, 3), generator=_gen(31), device=DEV).int()
+    u = torch.rand(50, 4, generator=_gen(32), device=DEV)
+    r = w.accept_draft(x, tokens, u, draft_logits=x[:, :3])
+    assert (r.count == 4).all() and torch.equal(r.tokens[:, :3], tokens)
+
+
+@pytest.mark.parametrize("dtype,mask", [(d, m) for d in DT for m in (-1e4, -1e9, -1e10, -1e25, "lowest")
+                                        if d != "fp16" or m in (-1e4, "lowest")])
+@pytest.mark.parametrize("t", [0.05, 4.0])
+def test_accept_masks_that_are_finite(cuda_device, dtype, mask, t):
+    """Tokens masked with a large negative logit, whole runs of them, are never drawn."""
+    B, V = 40, 9001
+    x = torch.randn(B, 3, V, generator=_gen(33), device=DEV).to(DT[dtype])
+    allowed = torch.zeros(V, dtype=torch.bool, device=DEV)
+    allowed[5::7] = True
+    allowed[1000:6000] = False
+    x[:, :, ~allowed] = torch.finfo(DT[dtype]).min if mask == "lowest" else mask
+    q = torch.randn(B, 2, V, generator=_gen(34), device=DEV).to(DT[dtype])
+    tokens = torch.randint(0, V, (B, 2), generator=_gen(35), device=DEV).int()
+    u = torch.rand(B, 3, generator=_gen(36), device=DEV)
+    status = w.new_status(DEV)
+    r = w.accept_draft(x, tokens, u, draft_logits=q, temperature=torch.full((B,), t, device=DEV), status=status)
+    assert int(status.item()) == 0
+    out = r.tokens[r.tokens >= 0].long()
+    assert allowed[out].all() and (r.count >= 1).all()
+    temps = torch.full((B,), t, device=DEV)
+    ids = tokens[:, :1].contiguous()
+    _check_rows(x[:3, 0].contiguous(), ids[:3], 5, temps[:3], w.token_logprobs(x[:3, 0].contiguous(), ids[:3], top_k=5,
+                                                                               temperature=temps[:3]))
 
 
 def test_accept_broadcast_and_refusals(cuda_device):

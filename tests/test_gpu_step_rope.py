@@ -142,6 +142,22 @@ def test_slots_outside_the_pool_write_nothing(cuda_device):
     assert torch.equal(q1, q2) and torch.equal(whole[0][5, :, 15], k2[1])
 
 
+def test_offsets_beyond_32_bits(cuda_device):
+    p, q, k, v, positions = _small()
+    p = w.params(4, 2, 64, page_size=256)
+    pages = 70000  # 2.3e9 elements a pool
+    pools = [torch.zeros(pages, 2, 256, 64, dtype=BF16, device=DEV) for _ in range(2)]
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    slots = torch.tensor([0, 255, pages * 256 - 1, pages * 256 - 256, 33333 * 256 + 7, 65535 * 256], device=DEV)
+    status = w.new_status(DEV)
+    _, ko = w.qk_norm_rope(p, None, q, k, v, positions, slots=slots, cache=w.PagedCache(*pools, table, table[0]),
+                           k_out=torch.empty(6, 2, 64, dtype=BF16, device=DEV), status=status)
+    assert int(status.item()) == 0 and torch.equal(ko, k)
+    for pool, new in zip(pools, (k, v)):
+        assert torch.equal(pool[slots // 256, :, slots % 256], new)
+        assert int(pool.count_nonzero()) == int(new.count_nonzero())
+
+
 def test_queries_or_keys_alone_in_place_and_verify_blocks(cuda_device):
     p, q, k, v, positions = _small()
     rope = w.Rope.from_frequencies(w.rope_frequencies(32), interleaved=True, device=DEV)
