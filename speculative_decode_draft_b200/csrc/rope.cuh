@@ -8,6 +8,15 @@
 // taken modulo 2^64, which drops whole turns exactly, and its upper 32 bits
 // are the fraction of a turn to 2^-32; far positions are as exact as near ones
 // (t * f in fp32 would be off by 0.06 rad at a million tokens).
+//
+// Bound by memory: each head row is read and written once, (in + 2) D bytes.
+// The instructions come close, so they are few: the cosines of a lane's four
+// pairs are worked out once for all rows of its slice, products go in packed pairs, and
+// heads of 64, 128 and 256 have kernels of their own without tests for the head's
+// end.  32768 tokens of 20 heads of 256 in bf16: 135 us, 5.0 TB/s, 76% of a
+// copy's rate (a warp per head row, angles worked out for each: 513 us); 4 blocks of
+// 64 registers per SM (3 of 80: 154 us), 2 rows in flight (1: 157, 4: 131 but 14.3
+// instead of 12.1 us for 1537 tokens).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -354,7 +354,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     device = logits.device
     logprobs = torch.empty(R, n, dtype=F32, device=device)
     entropy = torch.empty(R, dtype=F32, device=device)
-    lse = torch.empty(R, dtype=F32, device=device)
+    lse = torch.empty_like(entropy)
     top_logprobs = top_ids = None
     if top_k:
         top_logprobs = torch.empty(R, top_k, dtype=F32, device=device)
@@ -415,7 +415,7 @@ def accept_draft(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
     ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=device)
     tokens = torch.empty(B, n, dtype=I32, device=device)
     count = torch.empty(B, dtype=I32, device=device)
-    logprobs = torch.empty(B, n, dtype=F32, device=device)
+    logprobs = torch.empty_like(uniforms)
     L.check("wmtp_accept_draft", L.load().wmtp_accept_draft(
         B, n, V, dt, target_logits.data_ptr(), _row_stride(target_logits, 0), _row_stride(target_logits, 1),
         _ptr(draft_logits), *ds, draft_tokens.data_ptr(), uniforms.data_ptr(), _ptr(num_draft), _ptr(temperature),
