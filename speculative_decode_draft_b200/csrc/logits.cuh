@@ -422,6 +422,64 @@ struct TopShared {
   int listed, count;
 };
 
+// The keys of part_top where very many logits stand at its bound, `lowest`: those
+// above it, then the first columns at it, chunk by chunk until there are enough
+// (a row masked with -1e4 that leaves fewer than top_k tokens has its first masked
+// columns behind them).  Returns -1 if too many are above.
+template <typename T>
+__device__ __noinline__ int part_top_ties(const Part<T>& part, float lowest, int top_k, TopShared& sh, uint64_t* out) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  for (int i = part.v0 + tid; i < part.v1; i += kRowThreads) {
+    float x[N];
+    Vec<T>::unpack(part.load(i), x);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (!(x[j] > lowest)) continue;
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kMaxCandidates) sh.cand[at] = logit_key(x[j], part.col(i) + j);
+    }
+  }
+  __syncthreads();
+  const int above = sh.count;
+  if (above > kMaxCandidates) return -1;
+  for (int i = tid; i < above; i += kRowThreads) {
+    const uint64_t k = sh.cand[i];
+    int r = 0;
+    for (int j = 0; j < above; ++j) r += sh.cand[j] > k;
+    if (r < top_k) out[r] = k;
+  }
+  int n = above;
+  for (int base = part.v0; base < part.v1 && n < top_k; base += kRowThreads) {
+    float x[N];
+    int mine = 0;
+    Vec<T>::unpack(base + tid < part.v1 ? part.load(base + tid) : part.none(), x);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mine += x[j] == lowest;
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += u;
+    }
+    __syncthreads();
+    if (lane == 31) sh.cell[warp] = scan;
+    __syncthreads();
+    int at = n + scan - mine, total = 0;
+    for (int w = 0; w < kRowWarps; ++w) {
+      if (w < warp) at += sh.cell[w];
+      total += sh.cell[w];
+    }
+    for (int j = 0; j < N; ++j)
+      if (x[j] == lowest && at < top_k) out[at++] = logit_key(x[j], part.col(base + tid) + j);
+    n += total;
+  }
+  return min(n, top_k);
+}
+
 // The part's `top_k` largest keys, in order, to out[0 .. top_k), 0 behind the
 // last one.  Returns how many there are.
 //
@@ -431,7 +489,9 @@ struct TopShared {
 // bounds the part's top_k-th key from below, and what lies above it is in the cells
 // whose upper bound reaches it, about top_k of them: only these are read again
 // (from L2), and the few keys above the bound sorted by counting.  Should a list
-// overflow (a great many equal logits), the keys are taken one pass each.
+// overflow, logits equal to the bound are taken in order; the keys are taken one
+// pass each where even those above it are too many (one thread holds hundreds
+// of the largest logits).
 template <typename T>
 __device__ __forceinline__ int part_top(const Part<T>& part, const ThreadSum& z, int used, int shift, int top_k,
                                         TopShared& sh, uint64_t* out) {
@@ -489,11 +549,14 @@ __device__ __forceinline__ int part_top(const Part<T>& part, const ThreadSum& z,
     }
     n = min(n, top_k);
   } else {
-    uint64_t below = ~0ull;
-    for (n = 0; n < top_k; ++n) {
-      below = part_best<T>(part, below, sh.warp_best);
-      if (below == 0) break;
-      if (tid == 0) out[n] = below;
+    n = part_top_ties(part, lowest, top_k, sh, out);
+    if (n < 0) {
+      uint64_t below = ~0ull;
+      for (n = 0; n < top_k; ++n) {
+        below = part_best<T>(part, below, sh.warp_best);
+        if (below == 0) break;
+        if (tid == 0) out[n] = below;
+      }
     }
   }
   __syncthreads();

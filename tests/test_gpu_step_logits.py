@@ -151,6 +151,41 @@ def test_logprob_masked_and_extreme_rows(cuda_device):
     _check_rows(x[5:], tokens[5:], 3, None, w.token_logprobs(x[5:], tokens[5:], top_k=3))
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows", [2, 700])
+def test_logprob_top_tokens_among_very_many_equal_ones(cuda_device, dtype, rows):
+    """Fewer tokens than top_k above a plain of equal logits; a few in one thread's columns; a plain above all."""
+    V, top = 40003, 64
+    x = torch.full((rows, V), -1e4, device=DEV)
+    x[0, torch.randperm(V, generator=_gen(40), device=DEV)[:20]] = torch.randn(20, generator=_gen(41), device=DEV)
+    x[1, 8192 * torch.arange(4, device=DEV) + 3] = 2.0
+    if rows > 2:
+        x[2:] = torch.randn(rows - 2, V, generator=_gen(42), device=DEV)
+        x[2, 10000:20000] = 9.0
+        x[3, 5::2048] = 9.0
+        x[4] = NEG
+        x[4, 30000:30040] = 1.0
+        x[5] = NEG
+        x[5, 17:30000] = torch.finfo(DT[dtype]).min
+        x[6, 100:3000] = torch.linspace(20, 40, 2900, device=DEV)
+    x = x.to(DT[dtype])
+    tokens = torch.zeros(rows, 1, dtype=torch.int32, device=DEV)
+    r = w.token_logprobs(x, tokens, top_k=top)
+    for i in range(min(rows, 9)):
+        assert r.top_ids[i].tolist() == oracle.top_tokens(f64(x[i]), top), i
+
+
+def test_logprob_top_tokens_all_in_few_columns_of_a_stride(cuda_device):
+    """Thousands of the largest logits where one thread in 64 looks: every column of 8 in 2048."""
+    R, V = 1000, 131072
+    x = torch.randn(R, V, generator=_gen(43), device=DEV).bfloat16()
+    big = (torch.arange(V, device=DEV) % 2048) < 32
+    x[5, big] = (torch.rand(int(big.sum()), generator=_gen(44), device=DEV) * 50 + 10).bfloat16()
+    r = w.token_logprobs(x, torch.zeros(R, 1, dtype=torch.int32, device=DEV), top_k=64)
+    for i in (4, 5, 6):
+        assert r.top_ids[i].tolist() == oracle.top_tokens(f64(x[i]), 64)
+
+
 @pytest.mark.parametrize("t", [1e-30, 1e-6, 0.01, 100.0, 1e6, 1e30])
 @pytest.mark.parametrize("masked", [False, True])
 def test_logprob_extreme_temperatures(cuda_device, t, masked):
