@@ -791,17 +791,37 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) accept_rows_k
 constexpr unsigned kLeast = 0xc0df4000u;  // upper word of -32000.0
 constexpr double kNoWeight = 1e-250;
 __device__ __forceinline__ double lane_factor() { return exp2((threadIdx.x & 31) / 32.0); }
-__device__ __forceinline__ double exp_weight(double u, double factor) {
+template <int K>
+__device__ __forceinline__ void exp_weights(double (&u)[K], double factor) {  // step by step for all K: they overlap
   constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: rounds to whole numbers
   constexpr double c1 = 0.69314718055994530942 / 32, c2 = c1 * c1 / 2, c3 = c1 * c1 * c1 / 6, c4 = c1 * c1 * c1 * c1 / 24;
-  u = __hiloint2double(min(static_cast<unsigned>(__double2hiint(u)), kLeast), __double2loint(u));
-  const double kd = u + kMagic;
-  const int k = __double2loint(kd);
-  const double r = u - (kd - kMagic);
-  const double z = r * fma(r, fma(r, fma(r, c4, c3), c2), c1);
-  const double f = __shfl_sync(0xffffffffu, factor, k & 31);
-  const double e = fma(f, z, f);
-  return __hiloint2double(__double2hiint(e) + (k >> 5) * (1 << 20), __double2loint(e));
+  int k[K];
+  double z[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    u[i] = __hiloint2double(min(static_cast<unsigned>(__double2hiint(u[i])), kLeast), __double2loint(u[i]));
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const double kd = u[i] + kMagic;
+    k[i] = __double2loint(kd);
+    u[i] -= kd - kMagic;
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i) z[i] = fma(u[i], c4, c3);
+#pragma unroll
+  for (int i = 0; i < K; ++i) z[i] = fma(u[i], z[i], c2);
+#pragma unroll
+  for (int i = 0; i < K; ++i) z[i] = fma(u[i], z[i], c1);
+#pragma unroll
+  for (int i = 0; i < K; ++i) z[i] *= u[i];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const double f = __shfl_sync(0xffffffffu, factor, k[i] & 31);
+    u[i] = fma(f, z[i], f);
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    u[i] = __hiloint2double(__double2hiint(u[i]) + (k[i] >> 5) * (1 << 20), __double2loint(u[i]));
 }
 
 // The weights of the token that follows: p, or what p has above q (both not
@@ -815,12 +835,32 @@ struct FinalWeights {
   double pm, qm, scale;  // 32 log2(e) / T
   double r, factor;
   int drafted;  // -1: no draft to take away
-  __device__ __forceinline__ double pe(float x) const { return exp_weight((x - pm) * scale, factor); }
-  __device__ __forceinline__ double qe(float x) const { return exp_weight((x - qm) * scale, factor); }
-  __device__ __forceinline__ double operator()(float xp, float xq, int col) const {
-    const double e = pe(xp);
-    if (q == nullptr) return col == drafted ? 0.0 : e;
-    return fmax(e - r * qe(xq), 0.0);
+  // e: of p's logits; f: of q's.
+  template <int K>
+  __device__ __forceinline__ void pe(const float (&x)[K], double (&e)[K]) const {
+#pragma unroll
+    for (int i = 0; i < K; ++i) e[i] = (x[i] - pm) * scale;
+    exp_weights(e, factor);
+  }
+  template <int K>
+  __device__ __forceinline__ void qe(const float (&x)[K], double (&f)[K]) const {
+#pragma unroll
+    for (int i = 0; i < K; ++i) f[i] = (x[i] - qm) * scale;
+    exp_weights(f, factor);
+  }
+  // Of the columns col, col + step, ...
+  template <int K>
+  __device__ __forceinline__ void weights(const float (&xp)[K], const float (&xq)[K], int col, int step, double (&v)[K]) const {
+    pe(xp, v);
+    if (q != nullptr) {
+      double f[K];
+      qe(xq, f);
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = fmax(fma(-r, f[i], v[i]), 0.0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = col + i * step == drafted ? 0.0 : v[i];
+    }
   }
 };
 
@@ -831,33 +871,47 @@ __device__ __forceinline__ double warp_total(double v) {
 }
 
 constexpr int kFinalUnroll = 8;
+constexpr int kOverlap = 4;  // columns of a lane worked on at once
+constexpr int kLast = 2;  // columns of a lane in the last step of a draw
 
-// f(logit of p, logit of q, column) of the columns [c0, c1), a warp's; columns
-// behind c1 are masked.  32 columns at a time, kFinalUnroll loads in flight.
+// f(logits of p, logits of q, first column) for the columns [c0, c1), a warp's,
+// kOverlap at a time, 32 apart; columns behind c1 are masked.  kFinalUnroll
+// loads in flight.
 template <typename T, typename F>
 __device__ __forceinline__ void warp_columns(const T* p, const T* q, int c0, int c1, F f) {
   const int lane = threadIdx.x & 31;
-  int base = c0;
-  for (; base + 32 * kFinalUnroll <= c1; base += 32 * kFinalUnroll) {
-    float xp[kFinalUnroll], xq[kFinalUnroll];
+  for (int base = c0; base < c1; base += 32 * kFinalUnroll) {
+    float xp[kFinalUnroll / kOverlap][kOverlap], xq[kFinalUnroll / kOverlap][kOverlap];
+    if (base + 32 * kFinalUnroll <= c1) {
 #pragma unroll
-    for (int k = 0; k < kFinalUnroll; ++k) {
-      xp[k] = as_float(p[base + lane + 32 * k]);
-      xq[k] = q != nullptr ? as_float(q[base + lane + 32 * k]) : 0.f;
+      for (int k = 0; k < kFinalUnroll; ++k) {
+        const int c = base + lane + 32 * k;
+        xp[k / kOverlap][k % kOverlap] = as_float(p[c]);
+        xq[k / kOverlap][k % kOverlap] = q != nullptr ? as_float(q[c]) : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kFinalUnroll; ++k) {
+        const int c = base + lane + 32 * k;
+        xp[k / kOverlap][k % kOverlap] = c < c1 ? as_float(p[c]) : -INFINITY;
+        xq[k / kOverlap][k % kOverlap] = q != nullptr && c < c1 ? as_float(q[c]) : -INFINITY;
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kFinalUnroll; ++k) f(xp[k], xq[k], base + lane + 32 * k);
-  }
-  for (; base < c1; base += 32) {
-    const int c = base + lane;
-    f(c < c1 ? as_float(p[c]) : -INFINITY, q != nullptr && c < c1 ? as_float(q[c]) : -INFINITY, c);
+    for (int k = 0; k < kFinalUnroll; k += kOverlap)
+      if (base + 32 * k < c1) f(xp[k / kOverlap], xq[k / kOverlap], base + lane + 32 * k);
   }
 }
 
 template <typename T>
 __device__ __forceinline__ double warp_weight(const FinalWeights<T>& w, int c0, int c1) {
   double sum = 0.0;
-  warp_columns(w.p, w.q, c0, c1, [&](float xp, float xq, int col) { sum += w(xp, xq, col); });
+  warp_columns(w.p, w.q, c0, c1, [&](const float (&xp)[kOverlap], const float (&xq)[kOverlap], int col) {
+    double v[kOverlap];
+    w.weights(xp, xq, col, 32, v);
+#pragma unroll
+    for (int i = 0; i < kOverlap; ++i) sum += v[i];
+  });
   return warp_total(sum);
 }
 
@@ -1001,20 +1055,29 @@ __global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) 
   const int c1 = static_cast<int>(min(first + len, static_cast<long long>(a.V)));
   double all_p = 0.0, all_q = 0.0, over_p = 0.0, over_q = 0.0;
   if (minus) {
-    warp_columns(w.p, w.q, c0, c1, [&](float xp, float xq, int) {
-      const double e = w.pe(xp), f = w.qe(xq);
-      all_p += e;
-      all_q += f;
-      const bool over = e > w.r * f;
-      over_p += over ? e : 0.0;
-      over_q += over ? f : 0.0;
+    warp_columns(w.p, w.q, c0, c1, [&](const float (&xp)[kOverlap], const float (&xq)[kOverlap], int) {
+      double e[kOverlap], f[kOverlap];
+      w.pe(xp, e);
+      w.qe(xq, f);
+#pragma unroll
+      for (int i = 0; i < kOverlap; ++i) {
+        all_p += e[i];
+        all_q += f[i];
+        const bool over = e[i] > w.r * f[i];
+        over_p += over ? e[i] : 0.0;
+        over_q += over ? f[i] : 0.0;
+      }
     });
     all_q = warp_total(all_q), over_q = warp_total(over_q);
   } else {
-    warp_columns(w.p, w.q, c0, c1, [&](float xp, float, int col) {
-      const double e = w.pe(xp);
-      all_p += e;
-      over_p += col == w.drafted ? 0.0 : e;
+    warp_columns<T>(w.p, nullptr, c0, c1, [&](const float (&xp)[kOverlap], const float (&)[kOverlap], int col) {
+      double e[kOverlap];
+      w.pe(xp, e);
+#pragma unroll
+      for (int i = 0; i < kOverlap; ++i) {
+        all_p += e[i];
+        over_p += col + 32 * i == w.drafted ? 0.0 : e[i];
+      }
     });
   }
   all_p = warp_total(all_p), over_p = warp_total(over_p);
@@ -1046,16 +1109,16 @@ __global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) 
   double before;
   const int mine = sums.pick(want, &before);
   if (mine / kFinalWarps != rank) return;
-  // the run's CTA: a sixteenth of what is left to each warp, until one step of 32 columns is left
+  // the run's CTA: a sixteenth of what is left to each warp, until a lane's kLast columns are
   const long long lo = static_cast<long long>(mine) * len;
   int hi = static_cast<int>(min(lo + len, static_cast<long long>(a.V))), from = static_cast<int>(lo);
-  while (hi - from > 32) {
+  Running<1> part;
+  while (hi - from > kFinalThreads * kLast) {
     const int sub = (hi - from + 32 * kFinalWarps - 1) / (32 * kFinalWarps) * 32;
     const int s0 = min(from + warp * sub, hi), s1 = min(s0 + sub, hi);
     const double v = warp_weight(w, s0, s1);
     if (lane == 0) s_sub[warp] = v;
     __syncthreads();
-    Running<1> part;
     part.v[0] = lane < kFinalWarps ? s_sub[lane] : 0.0;
     __syncthreads();
     part.scan();
@@ -1064,12 +1127,24 @@ __global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) 
     before += skipped;
     hi = min(from + sub, hi);
   }
-  if (warp != 0) return;
-  const int c = from + lane;
-  Running<1> last;
-  last.v[0] = w(c < hi ? as_float(w.p[c]) : -INFINITY, c < hi && w.q != nullptr ? as_float(w.q[c]) : -INFINITY, c);
+  const int c = from + tid * kLast;
+  Running<kLast> last;
+  float xp[kLast], xq[kLast];
+#pragma unroll
+  for (int i = 0; i < kLast; ++i) {
+    xp[i] = c + i < hi ? as_float(w.p[c + i]) : -INFINITY;
+    xq[i] = c + i < hi && w.q != nullptr ? as_float(w.q[c + i]) : -INFINITY;
+  }
+  w.weights(xp, xq, c, 1, last.v);
   last.scan();
-  const int pick = min(from + last.pick(want - before, &before), a.V - 1);
+  if (lane == 0) s_sub[warp] = last.all;
+  __syncthreads();
+  part.v[0] = lane < kFinalWarps ? s_sub[lane] : 0.0;
+  part.scan();
+  double skipped;
+  const int at = part.pick(want - before, &skipped);
+  if (warp != at) return;
+  const int pick = min(from + warp * 32 * kLast + last.pick(want - before - skipped, &before), a.V - 1);
   if (lane == 0) {
     const size_t o = static_cast<size_t>(b) * n + d.k;
     a.tokens[o] = pick;
