@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -39,6 +40,30 @@ wmtp_status current_device(int* dev, DeviceInfo* info) {
   });
   if (g_dev[d].sms <= 0) return WMTP_ERR_CUDA;
   *info = g_dev[d];
+  return WMTP_OK;
+}
+
+// One attribute of one kernel, set once per device.  Only a success is
+// remembered: a failed attempt (its error cleared from this library's runtime
+// state) is retried by the next call.  Concurrent first calls from several host
+// threads serialise on the mutex.
+struct FuncAttrOnce {
+  std::atomic<bool> done[kMaxDevices];
+  std::mutex mu;
+};
+
+template <typename Kern>
+wmtp_status ensure_func_attr(FuncAttrOnce& once, Kern kern, cudaFuncAttribute attr, int value) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return WMTP_ERR_CUDA;
+  if (once.done[dev].load(std::memory_order_acquire)) return WMTP_OK;
+  std::lock_guard<std::mutex> lock(once.mu);
+  if (once.done[dev].load(std::memory_order_relaxed)) return WMTP_OK;
+  if (cudaFuncSetAttribute(kern, attr, value) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return WMTP_ERR_CUDA;
+  }
+  once.done[dev].store(true, std::memory_order_release);
   return WMTP_OK;
 }
 

@@ -39,8 +39,8 @@ constexpr int kRowCluster = 4;                     // most CTAs that share a row
 constexpr int kCells = 16;                         // of a thread, in the search for the largest logits
 constexpr int kMaxCells = 512;
 constexpr int kMaxCandidates = 1024;
-constexpr int kFinalCluster = 8;
-constexpr int kFinalThreads = 512;
+constexpr int kFinalCluster = 16;
+constexpr int kFinalThreads = 256;
 constexpr int kFinalWarps = kFinalThreads / 32;
 constexpr int kMaxTop = 64;
 
@@ -872,7 +872,7 @@ __device__ __forceinline__ double warp_total(double v) {
 
 constexpr int kFinalUnroll = 8;
 constexpr int kOverlap = 4;  // columns of a lane worked on at once
-constexpr int kLast = 2;  // columns of a lane in the last step of a draw
+constexpr int kLast = 4;  // columns of a lane in the last step of a draw
 
 // f(logits of p, logits of q, first column) for the columns [c0, c1), a warp's,
 // kOverlap at a time, 32 apart; columns behind c1 are masked.  kFinalUnroll
@@ -953,15 +953,16 @@ struct Running {
 };
 
 // One cluster per sequence.  Bound by the 64-bit units and, for few sequences, by
-// the latency of its steps: 32 sequences of 5 drafts and 129281 tokens take 23 us here
-// after 20 in the rows' pass, 1 of 3 drafts and 131072 tokens 9 after 5.
+// the latency of its steps: 32 sequences of 5 drafts and 129281 tokens take 19 us here
+// after 18 in the rows' pass (3 to decide, 11 for the weights, 5 to pick), 1 of 3
+// drafts and 131072 tokens 8 after 5.
 //
 // The weights' sums take one pass: p_i - r q_i is above 0 for the same i whether
 // r is exact or from the rows' fp32 sums, but for those within 1e-7 of 0; so the sums
 // of p, of q, and of both over the i with a weight give the exact r and with it
 // each run's sum.
 template <typename T>
-__global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) {
+__global__ void __launch_bounds__(kFinalThreads, 4) accept_kernel(AcceptArgs a) {
   constexpr int kMost = kFinalCluster * kFinalWarps, kPer = kMost / 32;
   __shared__ double s_sum[4][kMost];  // of each warp's run: p, q, p and q where there is a weight
   __shared__ double s_sub[kFinalWarps];
@@ -1109,7 +1110,7 @@ __global__ void __launch_bounds__(kFinalThreads, 2) accept_kernel(AcceptArgs a) 
   double before;
   const int mine = sums.pick(want, &before);
   if (mine / kFinalWarps != rank) return;
-  // the run's CTA: a sixteenth of what is left to each warp, until a lane's kLast columns are
+  // the run's CTA: an equal share of what is left to each warp, until kLast columns to a lane are
   const long long lo = static_cast<long long>(mine) * len;
   int hi = static_cast<int>(min(lo + len, static_cast<long long>(a.V))), from = static_cast<int>(lo);
   Running<1> part;

@@ -64,12 +64,13 @@ int row_cluster(long long rows, int vocab, int bytes, int sms) {
   return c;
 }
 
-// CTAs per sequence for the token that follows.  Device time in us of the whole call
-// with 2, 4, 8: 1 sequence of 3 drafts 24.8, 18.3, 14.9; 32 of 5 68.7, 61.9, 53.3;
-// 16 of 8 45.1, 34.7, 30.3.
+// CTAs per sequence for the token that follows: few of them of each sequence meet on
+// one SM.  Device time in us of the whole call with 8 of 512 threads and 16 of 256: 1
+// sequence of 3 drafts 13.5 and 12.5; 32 of 5 40.5 and 36.9; 16 of 8 29.6 and 29.0; with
+// fewer of 512 (2, 4 and 8, before other steps) 68.7, 61.9 and 53.3 for the 32.
 int final_cluster(long long batch, int vocab, int sms) {
   int c = 1;
-  while (c < kFinalCluster && batch * c < 2LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;
+  while (c < kFinalCluster && batch * c < 4LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;
   return c;
 }
 
@@ -297,6 +298,9 @@ wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32
   if (s != WMTP_OK) return s;
   c = final_cluster(batch, vocab, info.sms);
   auto kern = by_dtype(dtype, accept_kernel<float>, accept_kernel<__half>, accept_kernel<__nv_bfloat16>);
+  static FuncAttrOnce once[3];  // clusters of 16
+  s = ensure_func_attr(once[dtype], kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (s != WMTP_OK) return s;
   return launch_clusters(true, kern, dim3(static_cast<unsigned>(batch) * c), dim3(kFinalThreads), c, st, a);
 }
 

@@ -30,28 +30,10 @@ constexpr int kMaxVerifyWaves = 8;      // CTAs per SM in turn for the tcgen05 v
 constexpr int kMinTilesPerSplit = 16;   // extra waves only while full-capacity splits keep this many tiles
 
 // ---------------------------------------------------------------- launches
-// Dynamic shared-memory opt-in of one kernel, set once per device.  Only a
-// success is remembered: a failed attempt (its error cleared from this
-// library's runtime state) is retried by the next call.  Concurrent first
-// calls from several host threads serialise on the mutex.
-struct SmemAttrOnce {
-  std::atomic<bool> done[kMaxDevices];
-  std::mutex mu;
-};
-
+// Dynamic shared-memory opt-in of one kernel.
 template <typename Kern>
-wmtp_status ensure_smem_attr(SmemAttrOnce& once, Kern kern, int bytes) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return WMTP_ERR_CUDA;
-  if (once.done[dev].load(std::memory_order_acquire)) return WMTP_OK;
-  std::lock_guard<std::mutex> lock(once.mu);
-  if (once.done[dev].load(std::memory_order_relaxed)) return WMTP_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return WMTP_ERR_CUDA;
-  }
-  once.done[dev].store(true, std::memory_order_release);
-  return WMTP_OK;
+wmtp_status ensure_smem_attr(FuncAttrOnce& once, Kern kern, int bytes) {
+  return ensure_func_attr(once, kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -188,7 +170,7 @@ wmtp_status launch_decode_t(const CUtensorMap& tk, const CUtensorMap& tv, const 
   constexpr int alloc = SmemPlan<D, NT, S>::kAlloc;
   static_assert(alloc <= kSmemLimit, "shared-memory plan exceeds the sm_100 per-block limit");
   auto kern = decode_attn_kernel<D, NT, S, RING>;
-  static SmemAttrOnce once;
+  static FuncAttrOnce once;
   const wmtp_status s = ensure_smem_attr(once, kern, alloc);
   if (s != WMTP_OK) return s;
   return launch_programmatic(kern, dim3(a.nsplit, a.Hkv, B), kThreads, alloc, st, tk, tv, a);
@@ -214,7 +196,7 @@ wmtp_status launch_verify_tc_t(const CUtensorMap& tk, const CUtensorMap& tv, con
   constexpr int alloc = TcPlan<kTcKStages, kTcVStages, M == 64>::kAlloc;
   static_assert(alloc <= kSmemLimit, "shared-memory plan exceeds the sm_100 per-block limit");
   auto kern = verify_tc_kernel<kTcKStages, kTcVStages, M>;
-  static SmemAttrOnce once;
+  static FuncAttrOnce once;
   const wmtp_status s = ensure_smem_attr(once, kern, alloc);
   if (s != WMTP_OK) return s;
   return launch_programmatic(kern, dim3(a.nsplit, a.Hkv, B), kTcThreads, alloc, st, tk, tv, a);
