@@ -13,7 +13,7 @@
 // sequences.  More take two launches over all SMs: every block works the prefix
 // sums out for itself and moves its share of the pages, and the slot map follows, which
 // also writes what the first kernel's blocks still read, lengths and count.
-// A call takes 2.8 us for 4 sequences and 4 tokens each, 13 us for 512 sequences, 17,000
+// A call takes 2.8 us for 4 sequences and 4 tokens each, 12.6 us for 512 sequences, 17,000
 // pages and a map of 1,048,579 rows (12.6 MB, 2 us of a copy's rate).
 #pragma once
 
@@ -26,7 +26,7 @@ namespace wmtp {
 constexpr int kFewSeqs = 32;
 constexpr int kFewTokens = 4096;
 constexpr int kFewThreads = 512;
-constexpr int kMoveThreads = 1024;
+constexpr int kMoveThreads = 512;
 constexpr int kMoveBlocks = 148;
 constexpr int kManyBlocks = 8;  // where the sums do not fit shared memory
 constexpr int kSlotThreads = 256;
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kFewThreads) pages_few_kernel(PagesArgs a) {
   if (tid < a.B && s_served[tid]) a.kv_len[tid] = a.new_len[tid];  // read as the old one by the moves
 }
 
-// Inclusive prefix sums of N values over the block's threads, on top of *carry;
-// *carry: with the block's totals added.
+// Inclusive prefix sums of N values over the block's threads (N warps at least),
+// on top of *carry; *carry: with the block's totals added.
 template <int N>
 __device__ __forceinline__ void block_scan(long long (&v)[N], long long (&carry)[N], long long (*s_warp)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,7 +192,8 @@ __device__ __forceinline__ void block_scan(long long (&v)[N], long long (&carry)
   if (lane == 31)
     for (int n = 0; n < N; ++n) s_warp[n][warp] = v[n];
   __syncthreads();
-  if (warp < N) s_warp[warp][lane] = warp_scan(s_warp[warp][lane]);
+  // lanes without a warp of their own carry the total on
+  if (warp < N) s_warp[warp][lane] = warp_scan(lane < static_cast<int>(blockDim.x >> 5) ? s_warp[warp][lane] : 0);
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < N; ++n) {
