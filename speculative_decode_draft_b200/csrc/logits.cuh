@@ -181,7 +181,7 @@ struct Part {
   }
   __device__ __forceinline__ uint4 load(int i) const {
     const int c = col(i);
-    if (c >= 0 && c + N <= V) return __ldg(reinterpret_cast<const uint4*>(p + c));
+    if (c >= 0 && c + N <= V) return *reinterpret_cast<const uint4*>(p + c);
     uint32_t w[4];
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -324,7 +324,7 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
     const uint4* v = reinterpret_cast<const uint4*>(part.p + part.col(i));
     auto fetch = [&](uint4 (&u)[kRowUnroll]) {
 #pragma unroll
-      for (int k = 0; k < kRowUnroll; ++k) u[k] = __ldg(v + k * kRowThreads);
+      for (int k = 0; k < kRowUnroll; ++k) u[k] = v[k * kRowThreads];
       v += kBatch;
     };
     fetch(u0);
