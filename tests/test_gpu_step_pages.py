@@ -1,6 +1,8 @@
 """pages_resize against the Python page model: every table, stack, length and
 slot equal."""
 
+from ctypes import byref, c_size_t
+
 import numpy as np
 import pytest
 import torch
@@ -116,6 +118,31 @@ def test_inconsistent_state(cuda_device):
     m = w.pages_resize(s.p, s.pool, s.table, s.len, _i32([22, 3]), max_tokens=4, status=status)
     assert int(status.item()) == L.DEV_PAGE_OOB
     assert m.slots.tolist() == [-1] * 4 and m.positions.tolist() == [20, 21, -1, -1]
+
+
+def test_map_in_buffers_of_any_alignment(cuda_device):
+    """Through the C ABI: positions and slots need the alignment of their elements only."""
+    lib, B, most = w.load(), 40, 5003
+    p = w.params(16, 2, 256, page_size=32)
+    pool = w.DevicePages.allocate(400, DEV)
+    model = oracle.PageModel(32, 400, [[-1] * 9] * B, [0] * B, pool.free.tolist())
+    table, kv_len = _i32(np.full((B, 9), -1)), _i32([0] * B)
+    new = np.random.default_rng(3).integers(0, 200, B)
+    cu = torch.empty(B + 1, dtype=torch.int32, device=DEV)
+    positions = torch.full((most + 2,), 7, dtype=torch.int32, device=DEV)
+    slots = torch.full((most + 2,), 7, dtype=torch.int64, device=DEV)
+    size = c_size_t(0)
+    new_len = _i32(new)
+    args = (byref(p), B, table.data_ptr(), 9, kv_len.data_ptr(), new_len.data_ptr())
+    out = (cu.data_ptr(), positions.data_ptr() + 4, slots.data_ptr() + 8, most)
+    assert lib.wmtp_pages_resize(*args, None, None, 400, *out, None, byref(size), None, None) == 0
+    ws = torch.empty(size.value, dtype=torch.uint8, device=DEV)
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.wmtp_pages_resize(*args, pool.free.data_ptr(), pool.count.data_ptr(), 400, *out, ws.data_ptr(), byref(size),
+                                 None, st) == 0
+    want = model.resize(new, most)
+    assert cu.tolist() == want[0] and positions.tolist() == [7] + want[1] + [7] and slots.tolist() == [7] + want[2] + [7]
+    assert kv_len.tolist() == model.kv_len and table.tolist() == model.table
 
 
 def test_empty_batch(cuda_device):

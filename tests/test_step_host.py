@@ -221,6 +221,21 @@ def test_wrappers_refuse_cpu_tensors():
         w.qk_norm_rope(p, None, None, None, None, i[:, 0])
 
 
+def test_wrappers_refuse_what_is_no_tensor_or_no_params():
+    x = torch.zeros(2, 8)
+    i = torch.zeros(2, 1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="logits"):
+        w.token_logprobs([[0.0]], i)
+    with pytest.raises((TypeError, ValueError)):
+        w.accept_draft(x[None], i[None, :, 0], None)
+    with pytest.raises(TypeError):
+        w.pages_resize(7, w.DevicePages.allocate(4, "cpu"), i, i[:, 0], i[:, 0])
+    with pytest.raises(TypeError, match="params"):
+        w.pages_resize(b"1234", w.DevicePages.allocate(4, "cpu"), i, i[:, 0], i[:, 0])
+    with pytest.raises(AttributeError):
+        w.pages_resize(w.params(4, 1, 64), None, i, i[:, 0], i[:, 0])
+
+
 def test_rope_turns_are_whole_turns_modulo_one():
     import math
     r = w.Rope.from_frequencies([2 * math.pi * 0.25, 2 * math.pi * 1.25, -2 * math.pi * 0.25, 0.0], device="cpu")
