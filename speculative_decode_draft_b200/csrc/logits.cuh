@@ -343,8 +343,9 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
   if (i < part.v1) cut();
   const float2 o = sums();
   z.r.s = o.x, z.r.a = o.y;
-  if (z.best == -INFINITY) {  // masked: no weight, but NaN stays
+  if (z.best == -INFINITY) {  // masked: no weight (kLowest has some from T = 1e28 on), but NaN stays
     z.r.m = -FLT_MAX;
+    if (o.x == o.x) z.r.s = z.r.a = 0.f;
   } else if (z.best > -1e29f && fabsf(z.r.m) < 1e29f && fabsf(z.r.m * c) < 1e6f && c > 1e-20f && c < 1e7f) {
     const float low = fmaf(z.r.m, c, -__fmul_rn(z.r.m, c)), f = exp2f(-low);
     z.r.s = f * o.x;
