@@ -2,9 +2,9 @@
 // most likely alternatives, and the acceptance of drafted tokens.
 //
 // One pass over a row keeps, per thread, an anchor m near the running maximum
-// and, with d = x - m and c = log2(e) / T,
-//   s = sum 2^(c d),   a = sum 2^(c d) d,
-// from which lse = m / T + ln s and entropy = ln s - a / (T s).
+// and, with t = c (x - m) and c = log2(e) / T,
+//   s = sum 2^t,   a = sum 2^t t,
+// from which lse = m / T + ln s and entropy = ln s - ln 2 a / s.
 //
 // A row is read once, by a cluster of up to 4 CTAs where there are few rows;
 // the parts' sums meet in the shared memory of the cluster's first CTA.
@@ -31,6 +31,7 @@ namespace wmtp {
 namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowUnroll = 4;                      // 16-byte loads of a thread's batch; two batches are in flight
@@ -61,6 +62,17 @@ __device__ __forceinline__ float at_least(float x, float lo) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
   return r;
+}
+
+// f(x - m) for a product or quotient f: by halves where the difference of two
+// finite logits passes fp32, whatever T makes of it.
+template <typename F>
+__device__ __forceinline__ float of_difference(float x, float m, F f) {
+  const float d = x - m;
+  return d > -INFINITY ? f(d) : 2.f * f(0.5f * x - 0.5f * m);
+}
+__device__ __forceinline__ float times_difference(float x, float m, float c) {
+  return of_difference(x, m, [c](float d) { return d * c; });
 }
 
 // Stands for lower logits and -inf in exponents, so that none is infinite.
@@ -205,12 +217,12 @@ struct RowSum {
   float m, s, a;
 };
 
-// Moves the sums to a larger m.  Where the factor is 0 a difference may be
+// Moves the sums to a larger m.  Where the factor is 0 the exponent may be
 // infinite; NaN in s stays.
 __device__ __forceinline__ void row_sum_raise(RowSum& r, float m, float c) {
-  const float d = r.m - m;
-  const float f = exp2_fast(d * c);
-  r.a = f * (r.a + d * r.s);
+  const float t = times_difference(r.m, m, c);
+  const float f = exp2_fast(t);
+  r.a = f * (r.a + t * r.s);
   r.s *= f;
   if (f == 0.f) r.a = r.s;
   r.m = m;
@@ -240,9 +252,9 @@ __device__ __noinline__ RowSum part_sums_extreme(const Part<T>& part, float c, f
     float x[Vec<T>::N];
     Vec<T>::unpack(part.load(i), x);
     for (int j = 0; j < Vec<T>::N; ++j) {
-      const float d = x[j] - best, e = exp2_fast(d * c);
+      const float t = times_difference(x[j], best, c), e = exp2_fast(t);
       r.s += e;
-      r.a += e == 0.f ? 0.f : e * d;
+      r.a += e == 0.f ? 0.f : e * t;
     }
   }
   return r;
@@ -349,7 +361,7 @@ __device__ __forceinline__ ThreadSum part_sums(const Part<T>& part, float c, flo
   } else if (z.best > -1e29f && fabsf(z.r.m) < 1e29f && fabsf(z.r.m * c) < 1e6f && c > 1e-20f && c < 1e7f) {
     const float low = fmaf(z.r.m, c, -__fmul_rn(z.r.m, c)), f = exp2f(-low);
     z.r.s = f * o.x;
-    z.r.a = f * (o.y - low * o.x) / c;
+    z.r.a = f * (o.y - low * o.x);
   } else {
     z.r = part_sums_extreme<T>(part, c, z.best);
   }
@@ -651,11 +663,11 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) logprob_kerne
     if (j != tid && in) x_id = as_float(p[id]);
     if (!in && id != -1) set_status(a.status, kDevTokenOob);
     a.logprobs[static_cast<size_t>(r) * a.num_tokens + j] =
-        bad ? NAN : (none || !in) ? -INFINITY : (x_id - sum.m) * inv_t - ln_s;
+        bad ? NAN : (none || !in) ? -INFINITY : times_difference(x_id, sum.m, inv_t) - ln_s;
   }
   if (tid == 0) {
     if (a.lse != nullptr) a.lse[r] = bad ? NAN : none ? -INFINITY : sum.m * inv_t + ln_s;
-    if (a.entropy != nullptr) a.entropy[r] = bad ? NAN : none ? 0.f : ln_s - inv_t * sum.a / sum.s;
+    if (a.entropy != nullptr) a.entropy[r] = bad ? NAN : none ? 0.f : ln_s - kLn2 * sum.a / sum.s;
   }
   // every part's list is in order: a key's place is its own in its list plus,
   // in each other list, the number of keys above it
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) logprob_kerne
     }
     if (place >= a.top_k) continue;
     a.top_ids[o + place] = key_col(key);
-    a.top_logprobs[o + place] = (key_logit(key) - sum.m) * inv_t - ln_s;
+    a.top_logprobs[o + place] = times_difference(key_logit(key), sum.m, inv_t) - ln_s;
   }
   for (int i = (bad ? 0 : have) + tid; i < a.top_k; i += kRowThreads) {  // places without a token
     a.top_ids[o + i] = -1;
@@ -1012,8 +1024,8 @@ __global__ void __launch_bounds__(kFinalThreads, 4) accept_kernel(AcceptArgs a) 
       float lp = 0.f;
       bool ok = false;
       if (lane < nd && in && !row_is_bad) {
-        const float y = (as_float(target[lane * a.target_row + id]) - ts.m) * inv_t;
-        const float qd = with_q ? expf((as_float(draft[lane * a.draft_row + id]) - ds.m) * inv_t) / ds.s : 1.f;
+        const float y = times_difference(as_float(target[lane * a.target_row + id]), ts.m, inv_t);
+        const float qd = with_q ? expf(times_difference(as_float(draft[lane * a.draft_row + id]), ds.m, inv_t)) / ds.s : 1.f;
         lp = y - logf(ts.s);
         ok = greedy ? id == ts.best : u * qd < expf(y) / ts.s;
       }
@@ -1031,7 +1043,7 @@ __global__ void __launch_bounds__(kFinalThreads, 4) accept_kernel(AcceptArgs a) 
         }
         if (greedy && !bad) {
           id = ts.best;
-          lp = (as_float(target[k * a.target_row + id]) - ts.m) * inv_t - logf(ts.s);
+          lp = times_difference(as_float(target[k * a.target_row + id]), ts.m, inv_t) - logf(ts.s);
         }
       }
       if (rank == 0 && lane < n && (lane != k || !draws)) {  // a drawn token is written where it is found
@@ -1150,7 +1162,9 @@ __global__ void __launch_bounds__(kFinalThreads, 4) accept_kernel(AcceptArgs a) 
   if (lane == 0) {
     const size_t o = static_cast<size_t>(b) * n + d.k;
     a.tokens[o] = pick;
-    if (a.logprobs != nullptr) a.logprobs[o] = (as_float(w.p[pick]) - d.pm) / temp - logf(d.ps);
+    if (a.logprobs != nullptr)
+      a.logprobs[o] =
+          of_difference(as_float(w.p[pick]), d.pm, [temp](float y) { return y / temp; }) - logf(d.ps);
   }
 }
 
