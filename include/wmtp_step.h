@@ -151,7 +151,8 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
  *   top: the top_k largest logits, larger first, equal ones by lower id.
  *   logits      : [rows][vocab] of dtype, `row_stride` elements between rows;
  *                 what lies behind `vocab` is not read into any result
- *   temperature : [rows] fp32, or NULL for 1; finite and above 0
+ *   temperature : [rows] fp32, or NULL for 1; finite, above 0, and log2(e) / T
+ *                 finite in fp32 too, which it is from 4.25e-39 on
  *   tokens      : [rows][num_tokens] int32.  -1: no token (logprob -inf); any
  *                 other id outside [0, vocab) too, and WMTP_DEV_TOKEN_OOB
  *   logprobs_out: [rows][num_tokens]; entropy_out, lse_out: [rows] or NULL
@@ -189,7 +190,7 @@ wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, cons
  *   uniforms  : [batch][num_q] fp32 in [0, 1)
  *   num_draft : [batch] int32 in [0, num_q - 1], or NULL for num_q - 1 (outside:
  *               WMTP_DEV_LEN_OOB, the sequence emits nothing)
- *   temperature : [batch] fp32, finite and >= 0, or NULL for 1
+ *   temperature : [batch] fp32, 0 or as for wmtp_token_logprobs, or NULL for 1
  *   tokens_out: [batch][num_q] int32, the emitted tokens, -1 behind them
  *   count_out : [batch] int32, how many: accepted + 1
  *   logprobs_out : [batch][num_q] fp32 or NULL: ln p_i of each emitted token (of

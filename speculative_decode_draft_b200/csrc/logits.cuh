@@ -576,15 +576,16 @@ __device__ __forceinline__ int part_top(const Part<T>& part, const ThreadSum& z,
   return n;
 }
 
-// A row's temperature: 1 / T, or NaN for one that is no temperature.
-__device__ __forceinline__ float inverse_temperature(const float* temperature, int row) {
-  const float t = temperature != nullptr ? temperature[row] : 1.f;
-  return (t > 0.f && t < INFINITY) ? 1.f / t : NAN;
+// 1 / T, or NaN for a T that is no temperature, or so low that log2(e) / T, which
+// the exponents are multiplied with, passes fp32 (below 4.25e-39).
+__device__ __forceinline__ float inverse_temperature(float t) {
+  const float inv_t = 1.f / t;
+  return t > 0.f && t < INFINITY && inv_t * kLog2e < INFINITY ? inv_t : NAN;
 }
 
 // NaN or +inf somewhere in the row, or no temperature.
 __device__ __forceinline__ bool row_bad(const RowSum& r, float inv_t) {
-  return !(r.s < INFINITY) || !(r.m < INFINITY) || !(inv_t > 0.f && inv_t < INFINITY);
+  return !(r.s < INFINITY) || !(r.m < INFINITY) || !(inv_t == inv_t);
 }
 
 struct LogprobArgs {
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) logprob_kerne
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int r = blockIdx.x / parts, tid = threadIdx.x;
   const T* p = static_cast<const T*>(a.logits) + r * a.row_stride;
-  const float inv_t = inverse_temperature(a.temperature, r), c = inv_t * kLog2e;
+  const float inv_t = inverse_temperature(a.temperature != nullptr ? a.temperature[r] : 1.f), c = inv_t * kLog2e;
   // the given tokens' logits, while the row is read
   const int32_t* ids = a.tokens + static_cast<size_t>(r) * a.num_tokens;
   int id = -1;
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) accept_rows_k
     const T* p = target ? static_cast<const T*>(a.target) + b * a.target_batch + i * a.target_row
                         : static_cast<const T*>(a.draft) + b * a.draft_batch + i * a.draft_row;
     const Part<T> part(p, a.V, rank, parts);
-    const float inv_t = greedy ? 1.f : (temp > 0.f && temp < INFINITY) ? 1.f / temp : NAN;
+    const float inv_t = greedy ? 1.f : inverse_temperature(temp);
     const float c = inv_t * kLog2e;
     const ThreadSum z = part_sums<T>(part, c, nullptr, 0, 0);
     RowSum sum = block_sums(z.r, c, s_part);

@@ -196,7 +196,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     """Log probabilities of ``tokens`` int32 ``[rows, n]`` under ``logits [rows, vocab]``, each row's entropy and
     log-sum-exp, and its ``top_k`` (up to 64) most likely tokens (``wmtp_token_logprobs``).
 
-    ``logits``: bf16, fp16 or fp32, rows any stride apart.  ``temperature`` fp32 ``[rows]``, above 0.
+    ``logits``: bf16, fp16 or fp32, rows any stride apart.  ``temperature`` fp32 ``[rows]``, above 0
+    (at least 4.25e-39).
     """
     if stream is not None:
         with _on(stream, logits):
@@ -221,7 +222,8 @@ def accept_draft(target_logits: torch.Tensor, draft_tokens: torch.Tensor, unifor
     ``target_logits [B, gamma + 1, vocab]`` (a verify block's), ``draft_tokens`` int32 ``[B, gamma]``,
     ``uniforms`` fp32 ``[B, gamma + 1]`` in [0, 1).  ``draft_logits [B, gamma, vocab]``: the distributions that
     the tokens were drawn from; None if each was its draft's only choice.  ``num_draft`` int32 ``[B]``: how many
-    were drafted, at most gamma.  ``temperature`` fp32 ``[B]``; 0 is greedy.
+    were drafted, at most gamma.  ``temperature`` fp32 ``[B]``, at least 4.25e-39; 0 is
+    greedy.
     """
     if stream is not None:
         with _on(stream, target_logits):

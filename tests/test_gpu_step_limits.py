@@ -141,3 +141,48 @@ def test_bad_rows_stay_bad_at_high_temperatures(cuda_device, bad, t):
     r = w.token_logprobs(x, torch.zeros(3, 1, dtype=torch.int32, device=DEV), top_k=1, temperature=_temps(3, t), status=status)
     assert int(status.item()) == L.DEV_LOGITS
     assert r.lse[1].isnan() and r.top_ids[:, 0].tolist() == [-1] * 3 and r.lse[::2].tolist() == [NEG] * 2
+
+
+LOW_BAD = [1e-45, 1e-39, 2.9e-39, 3e-39, 4e-39, 4.2e-39]  # 1 / T or log2(e) / T pass fp32
+
+
+@pytest.mark.parametrize("t", LOW_BAD)
+@pytest.mark.parametrize("vocab", [3, 5001, 131072])
+def test_temperatures_below_the_lowest_are_bad(cuda_device, t, vocab):
+    """Whatever the row holds: logits, or masked tokens alone."""
+    x = torch.randn(3, vocab, device=DEV)
+    x[1], x[2] = NEG, 0.0
+    status = w.new_status(DEV)
+    r = w.token_logprobs(x, torch.zeros(3, 1, dtype=torch.int32, device=DEV), top_k=2, temperature=_temps(3, t), status=status)
+    assert int(status.item()) == L.DEV_LOGITS
+    assert r.lse.isnan().all() and r.entropy.isnan().all() and r.logprobs.isnan().all() and r.top_logprobs.isnan().all()
+    assert (r.top_ids == -1).all()
+    status.zero_()
+    none = torch.zeros(3, 0, dtype=torch.int32, device=DEV)
+    a = w.accept_draft(x[:, None], none, torch.full((3, 1), 0.5, device=DEV), temperature=_temps(3, t), status=status)
+    assert int(status.item()) == L.DEV_LOGITS and (a.count == 0).all() and (a.tokens == -1).all()
+
+
+@pytest.mark.parametrize("t", [4.25e-39, 5e-39, 1.1e-38, 1.2e-38, 1e-30])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("vocab", [3, 5001, 131072])
+def test_lowest_temperatures(cuda_device, t, dtype, vocab):
+    """The largest logit has all the weight.  A log probability is (x - max) / T with three roundings: 1 / T is a normal
+    number although T is not."""
+    x = torch.full((3, vocab), -0.125, device=DEV)
+    x[0, vocab - 1] = x[1, 1] = 0.0
+    x[2] = NEG
+    x[2, 2] = 0.5
+    x = x.to(DT[dtype])
+    best = [vocab - 1, 1, 2]
+    ids = torch.tensor([[b, 0] for b in best], dtype=torch.int32, device=DEV)
+    status = w.new_status(DEV)
+    r = w.token_logprobs(x, ids, top_k=1, temperature=_temps(3, t), status=status)
+    assert r.top_ids[:, 0].tolist() == best and (r.logprobs[:, 0] == 0).all() and (r.entropy == 0).all()
+    want = -0.125 / float(_temps(1, t)[0])
+    assert np.abs(f64(r.logprobs[:2, 1]) - want).max() <= 3 * 2.0 ** -24 * abs(want) and r.logprobs[2, 1] == NEG
+    drafts = torch.tensor([[best[0]], [0], [best[2]]], dtype=torch.int32, device=DEV)
+    a = w.accept_draft(x[:, None].expand(3, 2, vocab), drafts, torch.full((3, 2), 0.75, device=DEV),
+                       temperature=_temps(3, t), status=status)
+    assert int(status.item()) == 0
+    assert a.tokens.tolist() == [[best[0]] * 2, [1, -1], [2, 2]] and (a.logprobs == 0).all()
