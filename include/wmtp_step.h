@@ -13,7 +13,8 @@
  * The conventions of wmtp.h hold for every call here: device pointers owned by
  * the caller, nothing allocated, asynchronous on `stream` as a programmatic
  * dependent of the work before, host-detectable errors as a negative status
- * before anything is launched, device-detected ones as WMTP_DEV_* bits.
+ * before anything is launched, device-detected ones as WMTP_DEV_* bits.  An
+ * output overlaps no other buffer of its call, unless it is said below.
  * "Row" below is one distribution: `vocab` logits next to one another.
  */
 #ifndef WMTP_STEP_H_
@@ -83,7 +84,11 @@ typedef struct {
  *   q_out      : [tokens][num_heads_q][head_dim] bf16; may be q itself if q is
  *                contiguous bf16.  It is the attention calls' q.
  *   k_out      : [tokens][num_heads_kv][head_dim] bf16 or NULL: k_new of
- *                wmtp_ring_append and wmtp_verify_attn_append
+ *                wmtp_ring_append and wmtp_verify_attn_append.  May be k itself
+ *                if k is contiguous bf16.
+ * Tokens are encoded in any order.  A q_out or k_out that lies over rows of q, k
+ * or v in any other way, over the other one or over a pool is refused, and so are
+ * pools that overlap.  q, k and v may be rows of the pools that no token's slot is.
  *   rope       : NULL: no rotation
  * head_dim is a multiple of 8 in 8..256.
  */

@@ -39,6 +39,31 @@ bool heads_ok(const void* p, int64_t token_stride, int64_t head_stride, int byte
          head_stride * bytes % 16 == 0;
 }
 
+// Bytes next to one another, or rows of them in a [tokens][heads] view.
+struct Block {
+  __int128 at, bytes;  // at 0: absent
+  Block(const void* p, __int128 n) : at(reinterpret_cast<uintptr_t>(p)), bytes(n) {}
+  bool meets(const Block& o) const { return at != 0 && o.at != 0 && at < o.at + o.bytes && o.at < at + bytes; }
+};
+struct HeadRows {
+  Block row;  // the first one
+  __int128 tokens, heads, token_step, head_step;
+  bool meets(const Block& o) const {
+    const Block span(reinterpret_cast<const void*>(static_cast<uintptr_t>(row.at)),
+                     (tokens - 1) * token_step + (heads - 1) * head_step + row.bytes);
+    if (!span.meets(o)) return false;
+    for (__int128 h = 0; h < heads; ++h) {
+      const __int128 first = row.at + h * head_step;
+      // the first token whose row ends behind the block's start
+      const __int128 before = o.at - first - row.bytes;
+      const __int128 t = token_step == 0 || before < 0 ? 0 : before / token_step + 1;
+      const __int128 start = first + t * token_step;
+      if (t < tokens && start + row.bytes > o.at && start < o.at + o.bytes) return true;
+    }
+    return false;
+  }
+};
+
 template <typename F>
 F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
   return dtype == WMTP_FP32 ? fp32 : dtype == WMTP_FP16 ? fp16 : bf16;
@@ -120,6 +145,25 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
     return WMTP_ERR_INVALID_ARG;
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
     return WMTP_ERR_INVALID_ARG;
+  {
+    // Tokens are encoded in any order: no output may lie over what another token
+    // still reads or writes.  Rows that replace themselves may.
+    const __int128 T = tokens, row = 2LL * D;
+    const int Hq = params->num_heads_q, Hkv = params->num_heads_kv;
+    const HeadRows rq = {{q, D * bytes}, T, Hq, q_token_stride * bytes, q_head_stride * bytes};
+    const HeadRows rk = {{k, D * bytes}, T, Hkv, k_token_stride * bytes, k_head_stride * bytes};
+    const HeadRows rv = {{v, D * bytes}, T, Hkv, v_token_stride * bytes, v_head_stride * bytes};
+    const Block qo(q_out, T * Hq * row), ko(k_out, T * Hkv * row);
+    const __int128 pool = slots != nullptr ? static_cast<__int128>(kv->num_pages) * params->page_size * Hkv * row : 0;
+    const Block kp(slots != nullptr ? kv->k_pool : nullptr, pool), vp(slots != nullptr ? kv->v_pool : nullptr, pool);
+    auto same = [&](const void* x, const void* out, int heads, int64_t token, int64_t head) {
+      return x == out && bytes == 2 && (tokens == 1 || token == static_cast<int64_t>(heads) * D) && (heads == 1 || head == D);
+    };
+    if ((rq.meets(qo) && !same(q, q_out, Hq, q_token_stride, q_head_stride)) || rk.meets(qo) || rv.meets(qo) ||
+        (rk.meets(ko) && !same(k, k_out, Hkv, k_token_stride, k_head_stride)) || rq.meets(ko) || rv.meets(ko) ||
+        qo.meets(ko) || qo.meets(kp) || qo.meets(vp) || ko.meets(kp) || ko.meets(vp) || kp.meets(vp))
+      return WMTP_ERR_INVALID_ARG;
+  }
   RopeArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q, a.k = k, a.v = v;

@@ -120,7 +120,8 @@ def qk_norm_rope(p: L.Params, rope: Rope | None, q: torch.Tensor | None, k: torc
     or fp32, views cut from one packed projection too.  ``positions`` int32, one per token; a token with a
     negative position is padding and leaves everything as it was.  ``slots`` int64, one per token: where K and V
     go in ``cache``'s pools (``pages_resize`` makes both).  Without slots the keys are returned only (``v`` None).
-    ``k_out`` is None unless given or the only place for the keys.
+    ``k_out`` is None unless given or the only place for the keys.  ``q_out`` may be ``q`` and ``k_out`` ``k``
+    (contiguous, bf16); outputs that overlap q, k, v, one another or the pools otherwise are refused.
     """
     if stream is not None:
         with _on(stream, q if q is not None else k):
