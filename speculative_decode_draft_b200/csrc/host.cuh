@@ -67,6 +67,25 @@ wmtp_status ensure_func_attr(FuncAttrOnce& once, Kern kern, cudaFuncAttribute at
   return WMTP_OK;
 }
 
+// The widest cluster of one kernel on one device.  More than 8 CTAs are not
+// portable: a part of a GPU may have no place for them.  fits(): how many clusters
+// of `wide` CTAs the runtime says fit at once, negative if it failed, which is not
+// remembered.
+constexpr int kPortableCluster = 8;
+struct WidestOnce {
+  std::atomic<int> most[kMaxDevices];  // 0: not asked yet
+};
+
+template <typename Fits>
+int widest_cluster(WidestOnce& once, int dev, int wide, Fits fits) {
+  int most = once.most[dev].load(std::memory_order_acquire);
+  if (most != 0) return most;
+  const int n = fits();
+  most = n > 0 ? wide : kPortableCluster;
+  if (n >= 0) once.most[dev].store(most, std::memory_order_release);
+  return most;
+}
+
 // ---------------------------------------------------------------- launches
 // A launch whose success is read from the launch call itself, never from
 // cudaGetLastError (which would also report an unrelated earlier error left

@@ -93,10 +93,33 @@ int row_cluster(long long rows, int vocab, int bytes, int sms) {
 // one SM.  Device time in us of the whole call with 8 of 512 threads and 16 of 256: 1
 // sequence of 3 drafts 13.5 and 12.5; 32 of 5 40.5 and 36.9; 16 of 8 29.6 and 29.0; with
 // fewer of 512 (2, 4 and 8, before other steps) 68.7, 61.9 and 53.3 for the 32.
-int final_cluster(long long batch, int vocab, int sms) {
+int final_cluster(long long batch, int vocab, int sms, int most) {
   int c = 1;
-  while (c < kFinalCluster && batch * c < 4LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;
+  while (c < most && batch * c < 4LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;
   return c;
+}
+
+// Clusters of a kernel without dynamic shared memory that fit the device at once; -1:
+// the runtime does not say.
+template <typename Kern>
+int clusters_that_fit(Kern kern, int threads, int cluster) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = -1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return -1;
+  }
+  return n;
 }
 
 }  // namespace
@@ -340,11 +363,11 @@ wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32
       by_dtype(dtype, accept_rows_kernel<float>, accept_rows_kernel<__half>, accept_rows_kernel<__nv_bfloat16>);
   s = launch_clusters(true, rows_kern, dim3(rows * c), dim3(kRowThreads), c, st, a);
   if (s != WMTP_OK) return s;
-  c = final_cluster(batch, vocab, info.sms);
   auto kern = by_dtype(dtype, accept_kernel<float>, accept_kernel<__half>, accept_kernel<__nv_bfloat16>);
-  static FuncAttrOnce once[3];  // clusters of 16
-  s = ensure_func_attr(once[dtype], kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (s != WMTP_OK) return s;
+  static WidestOnce once[3];
+  c = final_cluster(batch, vocab, info.sms, widest_cluster(once[dtype], dev, kFinalCluster, [&] {
+                      return clusters_that_fit(kern, kFinalThreads, kFinalCluster);
+                    }));
   return launch_clusters(true, kern, dim3(static_cast<unsigned>(batch) * c), dim3(kFinalThreads), c, st, a);
 }
 
