@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 from ctypes import POINTER, c_float, c_int32, c_size_t, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,6 +35,13 @@ DTYPE_BF16 = 0
 DTYPE_FP16 = 1
 DTYPE_FP32 = 2
 WAIT_LIMIT_CYCLES = 4000000000  # WMTP_WAIT_LIMIT_CYCLES
+
+
+def binding_path() -> str:
+    """The compiled binding of the step calls, for this Python and this PyTorch."""
+    import torch
+    return os.path.join(HERE, f"_step_binding.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
 
 EXPORTS = (
     "wmtp_status_string",

@@ -14,7 +14,9 @@ share nothing.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
+import os
 from dataclasses import dataclass
 from typing import Sequence
 
@@ -33,13 +35,15 @@ def _binding():
     global _native
     if _native is None:
         lib = L.load()
-        try:
-            from . import _step_binding
-        except ImportError as e:
-            raise ImportError("_step_binding.so not found; build it with `python -m "
-                              "speculative_decode_draft_b200.build` (needs nvcc and a C++ compiler)") from e
-        _step_binding.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS))
-        _native = _step_binding
+        path = L.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} not found; build it with `python -m speculative_decode_draft_b200.build` (needs "
+                              "nvcc, a C++ compiler and the headers of Python and PyTorch)")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._step_binding", path)
+        binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(binding)
+        binding.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS))
+        _native = binding
     return _native
 
 
