@@ -306,8 +306,11 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& args, const RopeLane<I
   }
 }
 
+// Blocks that an SM holds at once of the kernel for chunks of `chunk` elements.
+__host__ __device__ constexpr int rope_blocks(int in_bytes, int chunk) { return chunk >= 4 || in_bytes == 4 ? 4 : 3; }
+
 template <typename In, int P, bool kInterleaved, int kLanes>
-__global__ void __launch_bounds__(kRopeThreads, P >= 4 || sizeof(In) == 4 ? 4 : 3) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, rope_blocks(sizeof(In), P)) rope_kernel(RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lanes = kLanes != 0 ? kLanes : a.lanes, lane = threadIdx.x & (lanes - 1), sub = (threadIdx.x & 31) & ~(lanes - 1);

@@ -70,11 +70,11 @@ F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
 }
 
 // Slices of a token's head rows, one for each group of lanes: as many as fit the
-// 32 warps that each SM holds at once; one where the tokens alone fill them, since each
+// warps that the SMs hold at once; one where the tokens alone fill them, since each
 // slice works its angles out again.  Device time in us of 20 rows of 256 with 1, 3, 10
 // slices: 16 tokens 8.6, 4.6, 3.2; 1537 15.2, 9.6, 13.6; 4096 21.0, 24.1, 32.4.
-int rope_slices(long long tokens, int rows, int lanes) {
-  const long long n = 148LL * 32 * 32 / lanes / tokens;
+int rope_slices(long long tokens, int rows, int lanes, long long warps) {
+  const long long n = warps * 32 / lanes / tokens;
   return n < 1 ? 1 : n < rows ? static_cast<int>(n) : rows;
 }
 
@@ -218,14 +218,18 @@ wmtp_status wmtp_qk_norm_rope(const wmtp_params* params, const wmtp_rope* rope, 
   a.inv_dim = 1.f / D;
   a.lanes = 1;
   while (a.lanes * 8 < D) a.lanes *= 2;
-  a.slices = rope_slices(tokens, rows, a.lanes);
+  const int half = a.rotary_dim / 2;
+  const int chunk = a.interleaved ? 16 / bytes : half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
+  int dev = 0;
+  DeviceInfo info;
+  const wmtp_status s = current_device(&dev, &info);
+  if (s != WMTP_OK) return s;
+  a.slices = rope_slices(tokens, rows, a.lanes, static_cast<long long>(info.sms) * rope_blocks(bytes, chunk) * kRopeWarps);
   a.per_slice = (rows + a.slices - 1) / a.slices;
   a.slices = (rows + a.per_slice - 1) / a.per_slice;
   const int groups = kRopeThreads / a.lanes;
   const long long grid = (static_cast<long long>(tokens) * a.slices + groups - 1) / groups;
   if (grid > kMaxGridX) return WMTP_ERR_UNSUPPORTED;
-  const int half = a.rotary_dim / 2;
-  const int chunk = half % 4 == 0 ? 4 : half % 2 == 0 ? 2 : 1;
   const int full = a.lanes * 8 == D ? a.lanes : 0;
   auto pick = [&](auto in) {
     using In = decltype(in);
