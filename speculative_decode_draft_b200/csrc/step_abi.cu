@@ -288,8 +288,11 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
   a.after = static_cast<int32_t*>(workspace), a.sums = a.after + seqs;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) return launch_plain(true, pages_few_kernel, dim3(1), dim3(kFewThreads), st, a);
-  const wmtp_status s =
-      launch_plain(true, pages_kernel, dim3(staged ? kMoveBlocks : kManyBlocks), dim3(kMoveThreads), st, a);
+  int dev = 0;
+  DeviceInfo info;
+  wmtp_status s = current_device(&dev, &info);
+  if (s != WMTP_OK) return s;
+  s = launch_plain(true, pages_kernel, dim3(static_cast<unsigned>(staged ? info.sms : kManyBlocks)), dim3(kMoveThreads), st, a);
   if (s != WMTP_OK) return s;
   const long long blocks = (max_tokens + 1LL * kSlotThreads * kSlotRows - 1) / (kSlotThreads * kSlotRows);
   return launch_plain(true, slots_kernel, dim3(static_cast<unsigned>(blocks > 0 ? blocks : 1)), dim3(kSlotThreads), st, a);
