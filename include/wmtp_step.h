@@ -15,7 +15,9 @@
  * dependent of the work before, host-detectable errors as a negative status
  * before anything is launched, device-detected ones as WMTP_DEV_* bits.  An
  * output overlaps no other buffer of its call, unless it is said below.
- * "Row" below is one distribution: `vocab` logits next to one another.
+ * "Row" below is one distribution: `vocab` logits next to one another.  Calls of
+ * the same sizes and alignment give the same bits.  A row's sums are split over more
+ * CTAs where there are few rows, so its last bits depend on how many the call has.
  */
 #ifndef WMTP_STEP_H_
 #define WMTP_STEP_H_
