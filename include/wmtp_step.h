@@ -168,6 +168,7 @@ wmtp_status wmtp_pages_resize(const wmtp_params* params, int32_t batch, int32_t*
  * A logit of -inf is a masked token of probability 0.  A row of them alone has
  * lse = -inf, entropy 0 and no token.  A row with NaN or +inf, or with a bad
  * temperature, is NaN throughout, ids -1, and sets WMTP_DEV_LOGITS.
+ * Sums are fp32, of terms that are good to 2^-22.
  */
 wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, const void* logits, int64_t row_stride,
                                 const float* temperature, const int32_t* tokens, int32_t num_tokens, int32_t top_k,
@@ -207,6 +208,9 @@ wmtp_status wmtp_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, cons
  * the tokens before it.
  *   workspace : as in wmtp_draft_attn_full (NULL: size query)
  * num_q in 1..32.  Masked tokens (top-k, top-p, a grammar) are -inf logits.
+ * p_i(d_i), q_i(d_i), their comparison and the log probabilities are fp32, from
+ * sums as in wmtp_token_logprobs: a u_i next to the border, within fp32's rounding
+ * of it, may fall on either side.  The draw's weights and sums are 64-bit.
  */
 wmtp_status wmtp_accept_draft(int32_t batch, int32_t num_q, int32_t vocab, int32_t dtype, const void* target,
                               int64_t target_batch_stride, int64_t target_row_stride, const void* draft,

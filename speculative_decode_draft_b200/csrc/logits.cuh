@@ -10,9 +10,9 @@
 // the parts' sums meet in the shared memory of the cluster's first CTA.
 //
 // Bound by memory, the special function unit (one 2^x a logit: 30 us for the
-// 1.3e8 logits below) and latency.  1024 rows of 131072 bf16: 51 us, 5.2 TB/s, 79% of
-// a copy's rate, and 59 with the 8 most likely tokens; the loads and maxima alone take
-// 47.  4 rows: 5.7 and 9 us, of which launch, joins and the search are most.
+// 1.3e8 logits below) and latency.  1024 rows of 131072 bf16: 50.5 us, 5.3 TB/s, 81% of
+// a copy's rate, and 58.5 with the 8 most likely tokens; the loads and maxima alone take
+// 47.  4 rows: 5.4 and 8.7 us, of which launch, joins and the search are most.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -971,8 +971,9 @@ struct Running {
 
 // One cluster per sequence.  Bound by the 64-bit units and, for few sequences, by
 // the latency of its steps: 32 sequences of 5 drafts and 129281 tokens take 19 us here
-// after 18 in the rows' pass (3 to decide, 11 for the weights, 5 to pick), 1 of 3
-// drafts and 131072 tokens 8 after 5.
+// after 17 in the rows' pass (3 to decide, 11 for the weights, 5 to pick), 1 of 3
+// drafts and 131072 tokens 8 after 4, 64 of one row each 35 in all.  64 registers spill
+// 64 bytes a thread.
 //
 // The weights' sums take one pass: p_i - r q_i is above 0 for the same i whether
 // r is exact or from the rows' fp32 sums, but for those within 1e-7 of 0; so the sums

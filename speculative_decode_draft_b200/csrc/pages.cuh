@@ -19,7 +19,7 @@
 // the device only and few do in a step, so the rule does not go by it; what that
 // costs is an end of many long requests in one call, at the worst (32 of 2^20
 // tokens on pages of 16) 2.6 ms against 30 us.
-// A call takes 2.8 us for 4 sequences and 4 tokens each, 12.6 us for 512 sequences, 17,000
+// Among others a call takes 2.6 us for 4 sequences and 4 tokens each, 12.6 us for 512 sequences, 17,000
 // pages and a map of 1,048,579 rows (12.6 MB, 2 us of a copy's rate).
 #pragma once
 

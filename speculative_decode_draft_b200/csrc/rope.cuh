@@ -13,10 +13,11 @@
 // The instructions come close, so they are few: the cosines of a lane's four
 // pairs are worked out once for all rows of its slice, products go in packed pairs, and
 // heads of 64, 128 and 256 have kernels of their own without tests for the head's
-// end.  32768 tokens of 20 heads of 256 in bf16: 135 us, 5.0 TB/s, 76% of a
-// copy's rate (a warp per head row, angles worked out for each: 513 us); 4 blocks of
-// 64 registers per SM (3 of 80: 154 us), 2 rows in flight (1: 157, 4: 131 but 14.3
-// instead of 12.1 us for 1537 tokens).
+// end.  32768 tokens of 20 heads of 256 in bf16: 133 us, 5.0 TB/s, 77% of a
+// copy's rate (a warp per head row, angles worked out for each: 513 us), interleaved
+// 138, in fp32 170, 90%; 4 blocks of 64 registers per SM (3 of 80: 152 us), 2 rows in
+// flight (1: 155, 4: 130 but 7.9 instead of 7.5 us for 1537 tokens).  64 registers
+// spill 36 to 108 bytes a thread, 248 for fp32 in chunks of 1.
 #pragma once
 
 #include <cuda_bf16.h>

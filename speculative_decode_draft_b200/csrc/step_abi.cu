@@ -72,7 +72,7 @@ F by_dtype(int32_t dtype, F fp32, F fp16, F bf16) {
 // Slices of a token's head rows, one for each group of lanes: as many as fit the
 // warps that the SMs hold at once; one where the tokens alone fill them, since each
 // slice works its angles out again.  Device time in us of 20 rows of 256 with 1, 3, 10
-// slices: 16 tokens 8.6, 4.6, 3.2; 1537 15.2, 9.6, 13.6; 4096 21.0, 24.1, 32.4.
+// slices: 16 tokens 8.5, 4.5, 3.1; 1537 10.2, 7.5, 12.0; 4096 17.6, 19.9, 29.1.
 int rope_slices(long long tokens, int rows, int lanes, long long warps) {
   const long long n = warps * 32 / lanes / tokens;
   return n < 1 ? 1 : n < rows ? static_cast<int>(n) : rows;
@@ -80,8 +80,8 @@ int rope_slices(long long tokens, int rows, int lanes, long long warps) {
 
 // CTAs that share each of `rows` rows: more while they are no more than five for
 // each SM (four are resident) and each keeps a whole batch.  Device time in us with
-// 1, 2, 4 CTAs a row of 131072 bf16, top 8: 4 rows 14.9, 12.1, 10.3; 300 rows 30.8,
-// 28.2, 35.3; 1024 rows 59.4, 73.6, 104.7.
+// 1, 2, 4 CTAs a row of 131072 bf16, top 8: 4 rows 14.6, 10.6, 8.7; 300 rows 32.4,
+// 30.8, 34.2; 1024 rows 58.4, 69.7, 92.8.  More than 4 were not tried.
 int row_cluster(long long rows, int vocab, int bytes, int sms) {
   int c = 1;
   const long long vecs = static_cast<long long>(vocab) * bytes / 16;
@@ -90,9 +90,8 @@ int row_cluster(long long rows, int vocab, int bytes, int sms) {
 }
 
 // CTAs per sequence for the token that follows: few of them of each sequence meet on
-// one SM.  Device time in us of the whole call with 8 of 512 threads and 16 of 256: 1
-// sequence of 3 drafts 13.5 and 12.5; 32 of 5 40.5 and 36.9; 16 of 8 29.6 and 29.0; with
-// fewer of 512 (2, 4 and 8, before other steps) 68.7, 61.9 and 53.3 for the 32.
+// one SM.  Device time in us of the whole call with at most 8 and 16: 1 sequence of 3
+// drafts 15.4 and 12.2; 32 of 5 48.4 and 36.4; 16 of 8 33.2 and 28.7.
 int final_cluster(long long batch, int vocab, int sms, int most) {
   int c = 1;
   while (c < most && batch * c < 4LL * sms && vocab / (2 * c) >= 4 * kFinalThreads) c *= 2;

@@ -201,7 +201,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top_k: int = 0
     """Log probabilities of ``tokens`` int32 ``[rows, n]`` under ``logits [rows, vocab]``, each row's entropy and
     log-sum-exp, and its ``top_k`` (up to 64) most likely tokens (``wmtp_token_logprobs``).
 
-    ``logits``: bf16, fp16 or fp32, rows any stride apart.  ``temperature`` fp32 ``[rows]``, above 0
+    ``logits``: bf16, fp16 or fp32, rows ``vocab`` elements apart or more.  ``temperature`` fp32 ``[rows]``, above 0
     (at least 4.25e-39).
     """
     if stream is not None:
